@@ -88,7 +88,8 @@ typedef enum rq_status {
 typedef enum rq_dtype {
     RQ_F32 = 0,   /* IEEE binary32 */
     RQ_BF16 = 1,  /* bfloat16 bit patterns (uint16) */
-    RQ_I32 = 2    /* raw int32 accumulators (rq_w4a4_linear output only) */
+    RQ_I32 = 2,   /* raw int32 accumulators (rq_w4a4_linear output only) */
+    RQ_I8 = 3     /* int8 codes with an fp32 scale (rq_kv_cache only) */
 } rq_dtype;
 
 /* Matrix cores that run an INT4 GEMM (rq_w4a4_linear_engine).
@@ -570,6 +571,209 @@ rq_status rq_w4a4_linear_engine(const rq_weight_header *hdr, const void *blob,
                                 const uint8_t *codes, const float *scale, const uint16_t *top,
                                 const uint8_t *codes_mma, int64_t T, const float *bias, void *Y,
                                 int32_t y_dtype, int32_t engine, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Attention between the rotated linears of a block: the QKV projection's
+ * output is normalized per head, rotated by position and stored in a paged
+ * key-value cache (rq_qk_norm_rope); one new token per sequence attends to
+ * its cache (rq_paged_attention); a cache over its budget drops the tokens
+ * that attention used least (rq_cache_evict).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * A paged key-value cache (host descriptor, device pointers).  Token j of
+ * sequence b ("slot j") lives in page table[b][j / page], offset j % page.
+ *   dtype     RQ_BF16, or RQ_I8: codes in [-127, 127] with one fp32 scale per
+ *             (token, head)
+ *   heads     key-value heads, 1 .. 1024
+ *   head_dim  D, 16 <= D <= 256, D % 8 == 0
+ *   page      slots of a page: a power of two, 16 .. 1024
+ *   batch     sequences (rows of table), 0 .. 65535
+ *   table_ld  pages of a sequence (columns of table), >= 1; table_ld * page
+ *             <= 2^24 slots
+ *   pages     pages that k and v hold, 1 .. 2^31 - 1
+ *   k, v      device [pages][heads][page][head_dim], 16-byte aligned
+ *   k_scale, v_scale  RQ_I8: device fp32 [pages][heads][page]; else NULL
+ *   table     device int32 [batch][table_ld].  An entry outside [0, pages)
+ *             means that no page is there: its slots are never read or
+ *             written and attention passes over them.
+ *   weight    device fp32 [batch][heads][table_ld * page] or NULL: the
+ *             attention weight each slot has received
+ *   pos       device int32 [batch][heads][table_ld * page] or NULL: the
+ *             position of the token in each slot (eviction reorders slots)
+ * No two sequences share a page that is written to (rq_qk_norm_rope,
+ * rq_cache_evict); reading shared pages is fine.
+ */
+typedef struct rq_kv_cache {
+    int32_t dtype;
+    int32_t heads;
+    int32_t head_dim;
+    int32_t page;
+    int32_t batch;
+    int32_t table_ld;
+    int64_t pages;
+    void *k;
+    void *v;
+    float *k_scale;
+    float *v_scale;
+    const int32_t *table;
+    float *weight;
+    int32_t *pos;
+} rq_kv_cache;
+
+/*
+ * Head norm and position rotation (host descriptor, device pointers).
+ *   q_heads, kv_heads  heads of the queries (1 .. 1024) and of the keys and
+ *             values (0 .. 1024; 0: queries only)
+ *   head_dim  D, 16 <= D <= 256, D % 8 == 0
+ *   rot_dim   leading coordinates that are rotated, 0 <= rot_dim <= D,
+ *             rot_dim % 8 == 0
+ *   interleaved  1: pairs (2i, 2i + 1); 0: pairs (i, i + rot_dim / 2)
+ *   table_rows  rows of cos and sin, >= 1 when rot_dim > 0
+ *   eps       added to the mean square, >= 0
+ *   q_weight, k_weight  device fp32 [D], or NULL for ones
+ *   cos, sin  device fp32 [table_rows][rot_dim / 2], 16-byte aligned (NULL
+ *             when rot_dim is 0)
+ */
+typedef struct rq_qk_norm {
+    int32_t q_heads;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t rot_dim;
+    int32_t interleaved;
+    int32_t table_rows;
+    float eps;
+    int32_t reserved;
+    const float *q_weight;
+    const float *k_weight;
+    const float *cos;
+    const float *sin;
+} rq_qk_norm;
+
+/*
+ * RMS norm of every query and key head with the position rotation, and the
+ * store of keys and values into a cache, in one pass.  Row t of qkv holds
+ * q_heads + kv_heads heads of D values, then (read only with a cache)
+ * kv_heads value heads.  For each query and key head x, fp32 throughout:
+ *   y[d] = x[d] / sqrt(mean(x^2) + eps) * weight[d]
+ *   (y[a], y[b]) <- (y[a] c - y[b] s, y[b] c + y[a] s) for pair i, with c, s =
+ *   cos, sin[positions[t]][i]
+ * rounded once, to the output's type or to the cache's.  Cache, RQ_I8: the
+ * symmetric 8-bit rule of rq_rotate_quant over the head's fp32 values: s =
+ * fl32(amax / 127), code = rne(fl32(y * fl32(127 / amax))); amax == 0 gives
+ * codes 0, s = 0.
+ * Arguments:
+ *   d          host descriptor
+ *   qkv        device [T][ld], dtype RQ_F32 or RQ_BF16
+ *   ld         elements from row to row, >= the row above
+ *   T          tokens, 0 <= T < 2^31
+ *   positions  device int32 [T] rows of cos and sin, NULL: row t.  A position
+ *              outside [0, table_rows) gives NaN in the rotated coordinates.
+ *   q_out      device, row t at t * q_ld: q_heads * D values of dtype.  May be
+ *              qkv itself with q_ld == ld (in place).
+ *   k_out      device, row t at t * k_ld: kv_heads * D values of dtype, or
+ *              NULL (with a cache or without key heads).  May be qkv +
+ *              q_heads * D with k_ld == ld.
+ *   cache      NULL, or the cache that receives keys and values (its heads and
+ *              head_dim are d's); its weight and pos, where given, are set to 0
+ *              and to the token's position (positions[t], or t)
+ *   seq        device int32 [T] sequence of each token, NULL: token t is of
+ *              sequence t
+ *   place      device int32 [T] slot of each token (cache given).  A token with
+ *              a negative place, a place past the table, a sequence outside
+ *              the batch or no page there is not stored.
+ *   Two tokens of one call must not share a (seq, place).
+ *   Row starts of qkv, q_out, k_out and cos, sin must be 16-byte aligned.
+ * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_DTYPE, RQ_ERR_ALIGN, RQ_ERR_HIP.
+ */
+rq_status rq_qk_norm_rope(const rq_qk_norm *d, const void *qkv, int32_t dtype, int64_t ld,
+                          int64_t T, const int32_t *positions, void *q_out, int64_t q_ld,
+                          void *k_out, int64_t k_ld, const rq_kv_cache *cache,
+                          const int32_t *seq, const int32_t *place, void *stream);
+
+/*
+ * Bytes of device workspace rq_paged_attention takes for this cache,
+ * q_heads, max_len and track.  It depends on these arguments and the
+ * device only, never on lengths or data.
+ * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_DTYPE.
+ */
+rq_status rq_paged_attention_workspace_bytes(const rq_kv_cache *cache, int32_t q_heads,
+                                             int64_t max_len, int32_t track, size_t *bytes);
+
+/*
+ * Attention of one new token per sequence over its cache.  For sequence b and
+ * query head i (of key-value head h = i / (q_heads / heads)), over the slots j
+ * < min(lens[b], max_len) that have a page and whose mask is not 0:
+ *   s_j = scale * sum_d q[d] k_j[d];  lse = log sum_j exp(s_j)
+ *   w_j = exp(s_j - lse);  out[d] = sum_j w_j v_j[d]
+ * Where no slot is left (length 0, all masked): out is 0 and lse -infinity.
+ * Keys and values of slots that are left out may hold anything, NaN included.
+ * Arguments:
+ *   cache      the cache; batch is the number of queries
+ *   q          device, row b at b * q_ld: q_heads * D values of dtype (RQ_F32
+ *              or RQ_BF16)
+ *   q_heads    a multiple of the cache's heads, at most 1024
+ *   scale      multiplies the scores (finite)
+ *   lens       device int32 [batch] tokens in the cache, the new one included
+ *              (values below 0 count as 0)
+ *   max_len    host bound of lens, 0 <= max_len <= table_ld * page; longer
+ *              sequences are cut to it
+ *   mask       device uint8 [batch], row b at b * mask_ld, or NULL: slots with
+ *              0 are left out; mask_ld >= max_len
+ *   out        device, row b at b * out_ld, dtype as q
+ *   lse        device fp32 [batch][q_heads] or NULL
+ *   track      1: add up the weights: weight_out[b][h][j] = weight[b][h][j] +
+ *              sum of w_j over h's query heads, for j < min(lens[b], max_len)
+ *              (slots past that are not written)
+ *   weight_out device fp32, shaped as the cache's weight and possibly the same
+ *              buffer; used with track only
+ *   workspace  device scratch of rq_paged_attention_workspace_bytes(), 16-byte
+ *              aligned
+ *   Rows of q and out must start 16-byte aligned.  out must not alias q.
+ * Sums and softmax statistics are fp32.  The same inputs give the same bits.
+ * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_DTYPE, RQ_ERR_ALIGN, RQ_ERR_HIP.
+ */
+rq_status rq_paged_attention(const rq_kv_cache *cache, const void *q, int32_t dtype, int64_t q_ld,
+                             int32_t q_heads, float scale, const int32_t *lens, int64_t max_len,
+                             const uint8_t *mask, int64_t mask_ld, void *out, int64_t out_ld,
+                             float *lse, int32_t track, float *weight_out, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/*
+ * Bytes of device workspace rq_cache_evict takes.
+ * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_DTYPE.
+ */
+rq_status rq_cache_evict_workspace_bytes(const rq_kv_cache *cache, int32_t keep, int64_t max_len,
+                                         size_t *bytes);
+
+/*
+ * Cuts every sequence longer than `keep` down to its `keep` best tokens, per
+ * key-value head.  Of the slots j < n = min(lens[b], max_len), those with pos <
+ * sink or pos > max pos - recent come first, the others by descending weight
+ * (NaN below everything); ties go to the lower slot.  The first `keep` stay.
+ * The places below `keep` that become free, ascending, receive the survivors
+ * from above, ascending: key, value, scales, weight and pos move; survivors
+ * below `keep` stay where they are, and slots from `keep` on keep their old
+ * contents.  (Attention does not depend on the order of the slots.)
+ * Arguments:
+ *   cache      the cache, with weight and pos; k, v and the scales are updated
+ *              in place.  A slot without a page moves weight and pos only.
+ *   lens       device int32 [batch]
+ *   max_len    host bound of lens, 0 <= max_len <= table_ld * page
+ *   keep       tokens that stay, >= 1
+ *   recent, sink  >= 0; positions are >= 0
+ *   lens_out   device int32 [batch]: min(n, keep); may be lens
+ *   weight_out, pos_out  shaped as the cache's weight and pos and possibly the
+ *              same buffers: slots below min(n, keep) are written, the others
+ *              not
+ *   workspace  device scratch of rq_cache_evict_workspace_bytes(), 16-byte
+ *              aligned
+ * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_DTYPE, RQ_ERR_ALIGN, RQ_ERR_HIP.
+ */
+rq_status rq_cache_evict(const rq_kv_cache *cache, const int32_t *lens, int64_t max_len,
+                         int32_t keep, int32_t recent, int32_t sink, int32_t *lens_out,
+                         float *weight_out, int32_t *pos_out, void *workspace,
+                         size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -104,4 +104,20 @@ int launch_gemm_codebook(const uint8_t *codes, const uint8_t *codes_mma, const f
                          const rq_weight_header *hdr, const void *blob, const float *bias,
                          void *Y, int y_dtype, void *stream);
 
+// Attention around the linears (rq_qknorm.hip, rq_attend.hip, rq_evict.hip);
+// arguments are validated by the caller (rq_attn_api.cpp).
+int launch_qk_norm_rope(const rq_qk_norm *d, const void *qkv, int bf16, int64_t ld, int64_t T,
+                        const int32_t *positions, void *q_out, int64_t q_ld, void *k_out,
+                        int64_t k_ld, const rq_kv_cache *cache, const int32_t *seq,
+                        const int32_t *place, void *stream);
+size_t attend_workspace_bytes(const rq_kv_cache *c, int q_heads, int64_t max_len, int track);
+int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_t q_ld, int q_heads,
+                           float scale, const int32_t *lens, int64_t max_len, const uint8_t *mask,
+                           int64_t mask_ld, void *out, int64_t out_ld, float *lse, int track,
+                           float *weight_out, void *workspace, void *stream);
+size_t evict_workspace_bytes(const rq_kv_cache *c, int keep, int64_t max_len);
+int launch_cache_evict(const rq_kv_cache *c, const int32_t *lens, int64_t max_len, int keep,
+                       int recent, int sink, int32_t *lens_out, float *weight_out,
+                       int32_t *pos_out, void *workspace, void *stream);
+
 }  // namespace rq

@@ -19,7 +19,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "librq.so")
 
 RQ_OK = 0
-RQ_F32, RQ_BF16, RQ_I32 = 0, 1, 2
+RQ_F32, RQ_BF16, RQ_I32, RQ_I8 = 0, 1, 2, 3
 RQ_ROT_RPBH, RQ_ROT_DENSE, RQ_ROT_TRDQ = 0, 1, 2
 RQ_Q_INT4_SYM, RQ_Q_LLOYDMAX, RQ_Q_INT4_ASYM, RQ_Q_MXFP4 = 0, 1, 2, 3
 RQ_ENGINE_AUTO, RQ_ENGINE_FP6, RQ_ENGINE_INT8 = 0, 1, 2
@@ -73,12 +73,31 @@ class c_set_header(ctypes.Structure):
 
 assert ctypes.sizeof(c_set_header) == 4864
 
+class c_kv_cache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("batch", ctypes.c_int32), ("table_ld", ctypes.c_int32),
+                ("pages", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("pos", ctypes.c_void_p)]
+
+
+class c_qk_norm(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("table_rows", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p)]
+
+
 # every symbol include/rq.h declares
 EXPORTS = ("rq_version", "rq_last_error", "rq_lloydmax_gaussian", "rq_packed_weight_bytes",
            "rq_pack_weights", "rq_rotate_quant_workspace_bytes", "rq_codes_mma_bytes",
            "rq_rotate_quant", "rq_w4a4_linear", "rq_w4a4_linear_engine",
            "rq_rotate_quant_noalloc", "rq_activation_bytes", "rq_weight_set_bytes",
-           "rq_pack_weight_set", "rq_weight_set_member")
+           "rq_pack_weight_set", "rq_weight_set_member", "rq_qk_norm_rope",
+           "rq_paged_attention_workspace_bytes", "rq_paged_attention",
+           "rq_cache_evict_workspace_bytes", "rq_cache_evict")
 
 _lib = None
 
@@ -111,11 +130,18 @@ def load() -> ctypes.CDLL:
     L.rq_pack_weight_set.argtypes = [P, I32, P, I32, P, P, I32, I32, P, SZ]
     L.rq_weight_set_member.argtypes = [P, I32, ctypes.POINTER(I32), ctypes.POINTER(P),
                                        ctypes.POINTER(I64)]
+    L.rq_qk_norm_rope.argtypes = [P, P, I32, I64, I64, P, P, I64, P, I64, P, P, P, P]
+    L.rq_paged_attention_workspace_bytes.argtypes = [P, I32, I64, I32, ctypes.POINTER(SZ)]
+    L.rq_paged_attention.argtypes = [P, P, I32, I64, I32, ctypes.c_float, P, I64, P, I64, P, I64,
+                                     P, I32, P, P, SZ, P]
+    L.rq_cache_evict_workspace_bytes.argtypes = [P, I32, I64, ctypes.POINTER(SZ)]
+    L.rq_cache_evict.argtypes = [P, P, I64, I32, I32, I32, P, P, P, P, SZ, P]
     for name in ("rq_lloydmax_gaussian", "rq_packed_weight_bytes", "rq_pack_weights",
                  "rq_rotate_quant_workspace_bytes", "rq_codes_mma_bytes", "rq_rotate_quant",
                  "rq_w4a4_linear", "rq_w4a4_linear_engine", "rq_rotate_quant_noalloc",
                  "rq_activation_bytes", "rq_weight_set_bytes", "rq_pack_weight_set",
-                 "rq_weight_set_member"):
+                 "rq_weight_set_member", "rq_qk_norm_rope", "rq_paged_attention_workspace_bytes",
+                 "rq_paged_attention", "rq_cache_evict_workspace_bytes", "rq_cache_evict"):
         getattr(L, name).restype = I32
     _lib = L
     return L
@@ -486,3 +512,226 @@ def w4a4_linear(dw: DeviceWeights, codes, scale, Y, top=None, bias=None, T=None,
         _check(load().rq_w4a4_linear(*args, _stream(stream)))
     else:
         _check(load().rq_w4a4_linear_engine(*args, ENGINES[engine], _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# attention around the linears
+# ---------------------------------------------------------------------------
+
+def _io_dtype(t) -> int:
+    import torch
+    if t.dtype is torch.bfloat16:
+        return RQ_BF16
+    if t.dtype is torch.float32:
+        return RQ_F32
+    raise TypeError(f"expected a float32 or bfloat16 tensor, got {t.dtype}")
+
+
+def _rows(t, n, width, name):
+    """Address and row stride of a 2-D (or [n][heads][D]) tensor of n rows of
+    width elements, each row contiguous."""
+    if t.dim() == 3:
+        if t.shape[1] * t.shape[2] != width or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+            raise ValueError(f"{name} must be rows of {width} contiguous elements")
+    elif t.dim() != 2 or t.shape[1] < width or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be rows of {width} contiguous elements")
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} rows, got {t.shape[0]}")
+    # (a single row has no stride to keep to)
+    return t.data_ptr(), t.stride(0) if n > 1 else max(width, t.shape[1] if t.dim() == 2 else width)
+
+
+def _vector(t, n, dtype, name):
+    """Address of a contiguous tensor of n elements (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements")
+    return t.data_ptr()
+
+
+def _on_device(device, **tensors):
+    import torch
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"the buffers are on {device}, which is not the current GPU")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+class KVCache:
+    """A paged key-value cache over the caller's tensors: k, v [pages][heads]
+    [page][D] (bfloat16, or int8 with fp32 k_scale, v_scale [pages][heads]
+    [page]), table int32 [batch][pages of a sequence] and, for eviction,
+    weight fp32 and pos int32 [batch][heads][pages of a sequence * page].
+    The tensors are held; replacing one needs a new KVCache."""
+
+    def __init__(self, k, v, table, k_scale=None, v_scale=None, weight=None, pos=None):
+        import torch
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must be [pages][heads][page][D] tensors of one shape and type")
+        if k.dtype not in (torch.bfloat16, torch.int8):
+            raise TypeError(f"the cache must be bfloat16 or int8, got {k.dtype}")
+        if not (k.is_contiguous() and v.is_contiguous()):
+            raise ValueError("k and v must be contiguous")
+        if table.dim() != 2 or table.dtype is not torch.int32 or not table.is_contiguous():
+            raise ValueError("table must be a contiguous int32 [batch][pages] tensor")
+        i8 = k.dtype is torch.int8
+        if i8 and (k_scale is None or v_scale is None):
+            raise ValueError("an int8 cache needs k_scale and v_scale")
+        if not i8 and (k_scale is not None or v_scale is not None):
+            raise ValueError("a bfloat16 cache has no scales")
+        pages, heads, page, D = k.shape
+        self.k, self.v, self.table, self.k_scale, self.v_scale = k, v, table, k_scale, v_scale
+        self.weight, self.pos = weight, pos
+        self.heads, self.head_dim, self.page, self.batch = heads, D, page, table.shape[0]
+        self.slots = table.shape[1] * page
+        self.device = k.device
+        for name, t in (("v", v), ("table", table), ("k_scale", k_scale), ("v_scale", v_scale),
+                        ("weight", weight), ("pos", pos)):
+            if t is not None and t.device != k.device:
+                raise ValueError(f"{name} is on {t.device}, not on {k.device}")
+        n = self.batch * heads * self.slots
+        self.c = c_kv_cache(
+            RQ_I8 if i8 else RQ_BF16, heads, D, page, self.batch, table.shape[1], pages,
+            k.data_ptr(), v.data_ptr(),
+            _vector(k_scale, pages * heads * page, torch.float32, "k_scale"),
+            _vector(v_scale, pages * heads * page, torch.float32, "v_scale"), table.data_ptr(),
+            _vector(weight, n, torch.float32, "weight"), _vector(pos, n, torch.int32, "pos"))
+        self._ref = ctypes.byref(self.c)
+
+    @staticmethod
+    def alloc(batch, heads, head_dim, max_len, page=64, int8=False, track=False, device="cuda"):
+        """An empty cache of its own pages, laid out sequence by sequence."""
+        import torch
+        per = -(-max_len // page)
+        shape = (max(1, batch * per), heads, page, head_dim)
+        new = lambda dt, *s: torch.zeros(*s, dtype=dt, device=device)  # noqa: E731
+        kind = torch.int8 if int8 else torch.bfloat16
+        table = torch.arange(batch * per, dtype=torch.int32, device=device).reshape(batch, per)
+        meta = (batch, heads, per * page)
+        return KVCache(new(kind, *shape), new(kind, *shape), table,
+                       new(torch.float32, *shape[:3]) if int8 else None,
+                       new(torch.float32, *shape[:3]) if int8 else None,
+                       new(torch.float32, *meta) if track else None,
+                       new(torch.int32, *meta) if track else None)
+
+
+class QKNorm:
+    """Head norm and position rotation: heads, weights fp32 [D] (None: ones),
+    cos and sin fp32 [rows][rot_dim / 2] (None: no rotation)."""
+
+    def __init__(self, q_heads, kv_heads, head_dim, q_weight=None, k_weight=None, cos=None,
+                 sin=None, eps=1e-6, interleaved=False):
+        import torch
+        self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
+        self.q_weight, self.k_weight, self.cos, self.sin = q_weight, k_weight, cos, sin
+        rows = half = 0
+        if cos is not None or sin is not None:
+            if cos is None or sin is None or cos.dim() != 2 or cos.shape != sin.shape:
+                raise ValueError("cos and sin must be [rows][rot_dim / 2] tensors of one shape")
+            rows, half = cos.shape
+        self.c = c_qk_norm(q_heads, kv_heads, head_dim, 2 * half, int(bool(interleaved)), rows,
+                           eps, 0, _vector(q_weight, head_dim, torch.float32, "q_weight"),
+                           _vector(k_weight, head_dim, torch.float32, "k_weight"),
+                           _vector(cos, rows * half, torch.float32, "cos"),
+                           _vector(sin, rows * half, torch.float32, "sin"))
+        self._ref = ctypes.byref(self.c)
+
+
+def qk_norm_rope(norm: QKNorm, qkv, q_out, k_out=None, positions=None, cache: KVCache = None,
+                 seq=None, place=None, stream=None):
+    """Head norm and rotation of the rows of qkv [T][heads * D], queries to
+    q_out, keys to k_out and/or with the values into the cache (slot place[t]
+    of sequence seq[t], or of sequence t).  q_out and k_out may be the parts
+    of qkv itself."""
+    import torch
+    T, D = int(qkv.shape[0]), norm.head_dim
+    dt = _io_dtype(qkv)
+    if q_out.dtype is not qkv.dtype or (k_out is not None and k_out.dtype is not qkv.dtype):
+        raise TypeError("q_out and k_out must have qkv's type")
+    qw, kw = norm.q_heads * D, norm.kv_heads * D
+    _on_device(qkv.device, q_out=q_out, k_out=k_out, positions=positions, seq=seq, place=place,
+               cache=cache, cos=norm.cos)
+    p_in, ld = _rows(qkv, T, qw + kw * (1 if cache is None else 2), "qkv")
+    p_q, q_ld = _rows(q_out, T, qw, "q_out")
+    p_k, k_ld = (None, 0) if k_out is None else _rows(k_out, T, kw, "k_out")
+    i32 = torch.int32
+    _check(load().rq_qk_norm_rope(
+        norm._ref, p_in, dt, ld, T, _vector(positions, T, i32, "positions"), p_q, q_ld, p_k, k_ld,
+        None if cache is None else cache._ref, _vector(seq, T, i32, "seq"),
+        _vector(place, T, i32, "place"), _stream(stream)))
+
+
+def paged_attention_workspace_bytes(cache: KVCache, q_heads: int, max_len: int, track=False) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().rq_paged_attention_workspace_bytes(cache._ref, q_heads, max_len, int(track),
+                                                     ctypes.byref(n)))
+    return n.value
+
+
+def paged_attention(q, cache: KVCache, lens, out, scale=None, max_len=None, mask=None, lse=None,
+                    track=False, weight_out=None, workspace=None, stream=None):
+    """Attention of q [batch][q_heads * D] over the cache: softmax of scale
+    (default 1 / sqrt(D)) times the scores over the first lens[b] slots whose
+    mask [batch][>= max_len] (uint8 or bool) is not 0.  lse fp32
+    [batch][q_heads].  track adds the weights to the cache's weight, written
+    to weight_out (default: in place)."""
+    import torch
+    B, D = cache.batch, cache.head_dim
+    dt = _io_dtype(q)
+    if out.dtype is not q.dtype:
+        raise TypeError("out must have q's type")
+    width = q.shape[1] if q.dim() == 2 else q.shape[1] * q.shape[2]
+    if width % D:
+        raise ValueError(f"a row of q must be whole heads of {D}, got {width}")
+    _on_device(q.device, cache=cache, lens=lens, out=out, mask=mask, lse=lse,
+               weight_out=weight_out, workspace=workspace)
+    p_q, q_ld = _rows(q, B, width, "q")
+    p_o, o_ld = _rows(out, B, width, "out")
+    if max_len is None:
+        max_len = cache.slots
+    p_m, m_ld = None, 0
+    if mask is not None:
+        if mask.dtype not in (torch.uint8, torch.bool):
+            raise TypeError("mask must be uint8 or bool")
+        p_m, m_ld = _rows(mask, B, max_len, "mask")
+    if track:
+        if cache.weight is None:
+            raise ValueError("track needs a cache with weight")
+        weight_out = cache.weight if weight_out is None else weight_out
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().rq_paged_attention(
+        cache._ref, p_q, dt, q_ld, width // D, D ** -0.5 if scale is None else scale,
+        _vector(lens, B, torch.int32, "lens"), max_len, p_m, m_ld, p_o, o_ld,
+        _vector(lse, B * (width // D), torch.float32, "lse"), int(track),
+        _vector(weight_out, B * cache.heads * cache.slots, torch.float32, "weight_out") if track else None,
+        None if workspace is None else workspace.data_ptr(), ws_bytes, _stream(stream)))
+
+
+def cache_evict_workspace_bytes(cache: KVCache, keep: int, max_len: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().rq_cache_evict_workspace_bytes(cache._ref, keep, max_len, ctypes.byref(n)))
+    return n.value
+
+
+def cache_evict(cache: KVCache, lens, keep, recent=0, sink=0, max_len=None, lens_out=None,
+                weight_out=None, pos_out=None, workspace=None, stream=None):
+    """Cut every sequence of the cache to its `keep` best tokens per head
+    (protected, then by weight); lens, weight and pos are updated in place
+    unless lens_out, weight_out and pos_out are given."""
+    import torch
+    B = cache.batch
+    if cache.weight is None or cache.pos is None:
+        raise ValueError("eviction needs a cache with weight and pos")
+    _on_device(cache.device, lens=lens, lens_out=lens_out, weight_out=weight_out, pos_out=pos_out,
+               workspace=workspace)
+    n = B * cache.heads * cache.slots
+    p_lens = _vector(lens, B, torch.int32, "lens")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().rq_cache_evict(
+        cache._ref, p_lens, cache.slots if max_len is None else max_len, keep, recent, sink,
+        p_lens if lens_out is None else _vector(lens_out, B, torch.int32, "lens_out"),
+        cache.c.weight if weight_out is None else _vector(weight_out, n, torch.float32, "weight_out"),
+        cache.c.pos if pos_out is None else _vector(pos_out, n, torch.int32, "pos_out"),
+        None if workspace is None else workspace.data_ptr(), ws_bytes, _stream(stream)))
