@@ -3,8 +3,8 @@
 //   s_j = scale q . k_j;  lse = log sum exp s_j;  out = sum exp(s_j - lse) v_j
 //
 // The cache is read once and nothing else is large, so HBM bounds it.  The
-// length is split into chunks, one workgroup per (chunk, key-value head,
-// sequence), joined by a second kernel where there is more than one chunk.
+// tokens of all sequences are dealt out to the workgroups in equal shares, and
+// a second kernel joins the parts of rows; short calls take one workgroup a row.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -34,16 +34,32 @@ struct Args {
     const uint8_t *mask;
     const float *weight;
     float *lse, *weight_out;
-    float *scores;   // [batch][q heads][score_ld], base-2 scores (tracked calls)
-    float *part;     // [batch][q heads][splits][D], unnormalized outputs of the chunks
-    float *stat;     // [batch][q heads][splits][2], their maxima and sums
+    float *scores;   // [rows][score_ld / 16][heads of a tile][16 slots], base-2 scores (tracked calls):
+                     // what a wave's store writes lies together
+    float *part;     // [workgroups + rows][heads of a tile][D], unnormalized outputs
+    float *stat;     // [workgroups + rows][heads of a tile][2], their maxima and sums
+    int64_t *first;  // [batch + 1]: steps of a head before each sequence; then steps of a workgroup
     int64_t q_ld, out_ld, mask_ld;
-    int32_t hq, G, max_len, chunk, splits, score_ld;
+    int32_t hq, G, tiles, tile_heads, max_len, score_ld, step_log;
     float scale2;    // scale * log2(e)
 };
 
 constexpr int kWaves = 4;      // waves of a workgroup
-constexpr int kTile = 32;      // tokens of one wave's step
+// 16-token blocks of one wave's step: 16 KB of keys and values of 128 dimensions
+// are in flight per wave for either type.  (int8 steps of 2 blocks took 5% longer
+// on 48 sequences of 4096 tokens; fp32 queries and D > 128 leave no registers for
+// 4.)
+constexpr int blocks_of(int DP, bool i8, bool bf16) { return i8 && bf16 && DP <= 128 ? 4 : 2; }
+// tokens of one workgroup's step
+constexpr int step_of(int DP, bool i8, bool bf16) { return kWaves * 16 * blocks_of(DP, i8, bf16); }
+constexpr int kLeastStep = kWaves * 32;
+constexpr int kThreads = kWaves * 64;
+constexpr int kMaxGroups = 1024;   // workgroups of a divided call, at most
+
+// waves of a SIMD, by the registers they need
+constexpr int resident(int DP, bool exact, bool bf16, bool i8) {
+    return DP == 256 ? 1 : DP == 128 ? (exact && bf16 && !i8 ? 3 : 2) : (bf16 && i8 ? 2 : 3);
+}
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const f2 v = {lo, hi};
@@ -68,6 +84,21 @@ __device__ __forceinline__ u4 widen8(u2 c) {
     const u2 a = widen4(c[0]), b = widen4(c[1]);
     return u4{a[0], a[1], b[0], b[1]};
 }
+constexpr float kLn2 = 0.69314718055994531f;
+template <bool BF16>
+__device__ __forceinline__ void store4(void *p, int64_t at, f4 v) {
+    if constexpr (BF16) *reinterpret_cast<u2 *>(static_cast<uint16_t *>(p) + at) = u2{pack2(v[0], v[1]), pack2(v[2], v[3])};
+    else *reinterpret_cast<f4 *>(static_cast<float *>(p) + at) = v;
+}
+// t[j] = the bytes j of a, b, c, d
+__device__ __forceinline__ void turn4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&t)[4]) {
+    const uint32_t ab = __builtin_amdgcn_perm(b, a, 0x05010400u), AB = __builtin_amdgcn_perm(b, a, 0x07030602u);
+    const uint32_t cd = __builtin_amdgcn_perm(d, c, 0x05010400u), CD = __builtin_amdgcn_perm(d, c, 0x07030602u);
+    t[0] = __builtin_amdgcn_perm(cd, ab, 0x05040100u);
+    t[1] = __builtin_amdgcn_perm(cd, ab, 0x07060302u);
+    t[2] = __builtin_amdgcn_perm(CD, AB, 0x05040100u);
+    t[3] = __builtin_amdgcn_perm(CD, AB, 0x07060302u);
+}
 // x as `parts` bf16 numbers whose sum carries 8 bits of x each
 template <int PARTS>
 __device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[PARTS]) {
@@ -79,7 +110,17 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[PARTS]) {
     }
 }
 
-// One chunk of one (sequence, key-value head, tile of 16 query heads).
+__device__ __forceinline__ int length_of(const Args &a, int b) { return min(max(a.lens[b], 0), a.max_len); }
+__device__ __forceinline__ int steps_of(const Args &a, int len) { return (int)((uint32_t)(len + (1 << a.step_log) - 1) >> a.step_log); }
+
+// A row is one (sequence, key-value head, tile of up to 16 query heads).
+//
+// DIRECT: one workgroup takes one row and writes its output.  Otherwise the
+// steps of all rows, in order, are dealt out in equal contiguous
+// shares: every workgroup is resident, starts once and ends with the others
+// whatever the lengths are.  A share can end and begin inside rows; the parts of
+// rows go to the workspace, part (workgroup + row), which no other pair shares
+// because along the shares one of the two grows from pair to pair.
 //
 // A wave takes 32 tokens a step, straight from memory into the operands of
 // v_mfma_f32_16x16x32_bf16, with no LDS:
@@ -97,23 +138,86 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[PARTS]) {
 // parts (24 bits).  Weights enter as two bf16 parts (2^-17) for bf16 outputs
 // and three for fp32: with one part their rounding would be as large as the
 // output's own.  Sums and statistics are fp32.
-template <int DP, bool EXACT, bool I8, bool BF16, bool MASKED, bool TRACK>
-__global__ void __launch_bounds__(kWaves * 64) attend_kernel(Args a) {
+template <int DP, bool EXACT, bool I8, bool BF16, bool MASKED, bool TRACK, bool DIRECT>
+__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(resident(DP, EXACT, BF16, I8)))) attend_kernel(Args a) {
     constexpr int QP = BF16 ? 1 : 3, PP = BF16 ? 2 : 3;
     constexpr int KS = DP / 32;                  // products along d
     constexpr int W = DP == 64 ? 4 : 8;          // d of one value load
     constexpr int NU = DP / (16 * W);            // value loads of a token
+    constexpr int H = blocks_of(DP, I8, BF16), TILE = 16 * H, STEP = step_of(DP, I8, BF16);
     __shared__ float s_m[kWaves][16], s_l[kWaves][16];
     __shared__ float s_o[kWaves][16][DP + 4];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g4 = lane >> 4;
-    const int tiles = (a.G + 15) / 16;
-    const int h = blockIdx.y / tiles, g0 = (blockIdx.y % tiles) * 16, b = blockIdx.z, sp = blockIdx.x;
-    const int len = min(max(a.lens[b], 0), a.max_len);
-    const int begin = sp * a.chunk, end = min(len, begin + a.chunk);
-    if (begin >= len && a.splits > 1) return;
     const int D = EXACT ? DP : a.c.D;
+    const int rows_of_seq = a.c.heads * a.tiles;
+
+    // this workgroup's steps [u, u_end), and the row that u lies in
+    int b, r, len;            // sequence; row of the sequence; its length
+    int64_t u = 0, u_end = 1;
+    int step0 = 0;            // first step within the row
+    if constexpr (DIRECT) {
+        b = blockIdx.x / rows_of_seq;
+        r = blockIdx.x - b * rows_of_seq;
+        len = length_of(a, b);
+    } else {
+        __shared__ int64_t s_wave[kWaves];
+        __shared__ int64_t s_at;
+        __shared__ int s_b, s_len;
+        const int each = (a.c.batch + kThreads - 1) / kThreads, lo = threadIdx.x * each, hi = min(lo + each, a.c.batch);
+        const int len0 = lo < hi ? length_of(a, lo) : 0;
+        int64_t mine = steps_of(a, len0);
+        for (int i = lo + 1; i < hi; ++i) mine += steps_of(a, length_of(a, i));
+        int64_t upto = mine;
+        for (int o = 1; o < 64; o *= 2) {
+            const int64_t y = __shfl_up(upto, o);
+            if (lane >= o) upto += y;
+        }
+        if (lane == 63) s_wave[wave] = upto;
+        __syncthreads();
+        int64_t all = 0;
+        for (int w = 0; w < kWaves; ++w) {
+            if (w < wave) upto += s_wave[w];
+            all += s_wave[w];
+        }
+        const int64_t per = max((int64_t)1, (all * rows_of_seq + gridDim.x - 1) / gridDim.x);
+        u = blockIdx.x * per;
+        u_end = min(all * rows_of_seq, u + per);
+        if (blockIdx.x == 0) {
+            int64_t at = upto - mine;
+            for (int i = lo; i < hi; ++i) {
+                a.first[i] = at;
+                at += steps_of(a, length_of(a, i));
+            }
+            if (threadIdx.x == 0) a.first[a.c.batch] = per;
+        }
+        if (u >= u_end) return;
+        if ((upto - mine) * rows_of_seq <= u && u < upto * rows_of_seq) {   // one thread
+            int64_t at = upto - mine;
+            int i = lo, n = len0;
+            while (u >= (at + steps_of(a, n)) * rows_of_seq) {
+                at += steps_of(a, n);
+                n = length_of(a, ++i);
+            }
+            s_b = i;
+            s_len = n;
+            s_at = at;
+        }
+        __syncthreads();
+        b = __builtin_amdgcn_readfirstlane(s_b);
+        const int64_t off = u - s_at * rows_of_seq;
+        len = __builtin_amdgcn_readfirstlane(s_len);
+        const int n = steps_of(a, len);
+        r = __builtin_amdgcn_readfirstlane((int)(off / n));
+        step0 = __builtin_amdgcn_readfirstlane((int)(off - (int64_t)r * n));
+    }
+
+    for (;;) {
+    const int row_steps = steps_of(a, len);
+    const int here = DIRECT ? row_steps : (int)min((int64_t)(row_steps - step0), u_end - u);
+    const int begin = step0 * STEP, end = min(len, begin + here * STEP);
+    const int h = r / a.tiles, g0 = (r - h * a.tiles) * 16;
     const int heads = min(16, a.G - g0);
     const int64_t head0 = (int64_t)b * a.hq + h * a.G + g0;
 
@@ -151,32 +255,31 @@ __global__ void __launch_bounds__(kWaves * 64) attend_kernel(Args a) {
     float m = -INFINITY, l = 0.0f;
 
     constexpr int EB = I8 ? 1 : 2;   // bytes of an element
-    const int steps = (end - begin + kWaves * kTile - 1) / (kWaves * kTile);
+    const int steps = here;
     const int page_mask = (1 << a.c.page_log) - 1;
 
-    // the pages of this wave's next 32 steps: lane 2 i + half
+    // the pages of this wave's next 64 / H steps: lane H i + block
     int32_t page_of = -1;
     auto load_pages = [&](int step) {
-        const int j = begin + ((step + (lane >> 1)) * kWaves + wave) * kTile + (lane & 1) * 16;
-        const int idx = j >> a.c.page_log;
-        page_of = j < end ? a.c.table[(int64_t)b * a.c.table_ld + idx] : -1;
+        const int j = begin + ((step + lane / H) * kWaves + wave) * TILE + (lane % H) * 16;
+        page_of = j < end ? a.c.table[(int64_t)b * a.c.table_ld + (j >> a.c.page_log)] : -1;
     };
-    // base row of half `hf` of a step; `there`: whether it has a page
-    auto row_of = [&](int step, int hf, bool &there) -> int64_t {
-        const int j = begin + (step * kWaves + wave) * kTile + hf * 16;
-        const int32_t pg = __builtin_amdgcn_readlane(page_of, (step & 31) * 2 + hf);
+    // base row of block x of a step; `there`: whether it has a page
+    auto row_of = [&](int step, int x, bool &there) -> int64_t {
+        const int j = begin + (step * kWaves + wave) * TILE + x * 16;
+        const int32_t pg = __builtin_amdgcn_readlane(page_of, (step & (64 / H - 1)) * H + x);
         there = (uint32_t)pg < (uint32_t)a.c.pages;
         return (((int64_t)(there ? pg : 0) * a.c.heads + h) << a.c.page_log) + (j & page_mask);
     };
 
-    u4 kreg[2][KS];
-    u4 vreg[8][NU];       // bf16: W / 2 dwords used; int8: W / 4
-    f4 ks[2], vs[2];
-    bool there[2], v_there[2];
+    u4 kreg[H][KS];
+    u4 vreg[H * 4][NU];   // bf16: W / 2 dwords used; int8: W / 4
+    f4 ks[H], vs[H];
+    bool there[H];
 
     auto load_k = [&](int step) {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
+        for (int hf = 0; hf < H; ++hf) {
             const int64_t row = row_of(step, hf, there[hf]);
             const char *base = static_cast<const char *>(a.c.k) + row * (D * EB);
 #pragma unroll
@@ -200,8 +303,9 @@ __global__ void __launch_bounds__(kWaves * 64) attend_kernel(Args a) {
     };
     auto load_v = [&](int step) {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            const int64_t row = row_of(step, hf, v_there[hf]);
+        for (int hf = 0; hf < H; ++hf) {
+            bool unused;
+            const int64_t row = row_of(step, hf, unused);
             const char *base = static_cast<const char *>(a.c.v) + row * (D * EB);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -222,20 +326,22 @@ __global__ void __launch_bounds__(kWaves * 64) attend_kernel(Args a) {
         }
     };
 
-    auto mine = [&](int step) { return begin + (step * kWaves + wave) * kTile < end; };   // wave-uniform
+    auto mine = [&](int step) { return begin + (step * kWaves + wave) * TILE < end; };   // wave-uniform
     if (mine(0)) {
         load_pages(0);
         load_k(0);
         load_v(0);
     }
     for (int step = 0; step < steps && mine(step); ++step) {
-        const int j0 = begin + (step * kWaves + wave) * kTile;
+        const int j0 = begin + (step * kWaves + wave) * TILE;
         const bool more = step + 1 < steps && mine(step + 1);
         // scores: lane (head col, g4) gets tokens j0 + 16 hf + 4 g4 + i
-        f4 s[2];
-        bool ok[2] = {there[0], there[1]};
+        f4 s[H];
+        bool ok[H];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
+        for (int hf = 0; hf < H; ++hf) ok[hf] = there[hf];
+#pragma unroll
+        for (int hf = 0; hf < H; ++hf) {
             s[hf] = f4{0, 0, 0, 0};
 #pragma unroll
             for (int t = 0; t < KS; ++t) {
@@ -252,17 +358,18 @@ __global__ void __launch_bounds__(kWaves * 64) attend_kernel(Args a) {
                 if constexpr (I8) s[hf][i] *= ks[hf][i];
             }
         }
-        const bool v_ok[2] = {v_there[0], v_there[1]};
         if (more) {
-            if (((step + 1) & 31) == 0) load_pages(step + 1);
+            if (((step + 1) & (64 / H - 1)) == 0) load_pages(step + 1);
             load_k(step + 1);
         }
         // tokens that are left out
-        bool whole = j0 + kTile <= end && ok[0] && ok[1] && !MASKED;
-        bool use[2][4];
+        bool whole = j0 + TILE <= end && !MASKED;
+#pragma unroll
+        for (int hf = 0; hf < H; ++hf) whole = whole && ok[hf];
+        bool use[H][4];
         if (!whole) {
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
+            for (int hf = 0; hf < H; ++hf)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int j = j0 + hf * 16 + g4 * 4 + i;
@@ -276,13 +383,14 @@ __global__ void __launch_bounds__(kWaves * 64) attend_kernel(Args a) {
         if constexpr (TRACK) {
             if (col < heads)
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf)
-                    *reinterpret_cast<f4 *>(a.scores + (head0 + col) * a.score_ld + j0 + hf * 16 + g4 * 4) = s[hf];
+                for (int hf = 0; hf < H; ++hf)
+                    *reinterpret_cast<f4 *>(a.scores + (((int64_t)b * rows_of_seq + r) * a.score_ld + j0 + hf * 16) * a.tile_heads + col * 16 + g4 * 4) = s[hf];
         }
         // The running maximum only moves when a score passes it by 2^8: weights
         // up to 256 are as exact, and most steps leave the sums as they are.
-        float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                          fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+        float top = -INFINITY;
+#pragma unroll
+        for (int hf = 0; hf < H; ++hf) top = fmaxf(top, fmaxf(fmaxf(s[hf][0], s[hf][1]), fmaxf(s[hf][2], s[hf][3])));
         if (__any(top > m + 8.0f)) {
             top = fmaxf(max_of_four(top), m);
             const float f = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - top);
@@ -294,53 +402,66 @@ __global__ void __launch_bounds__(kWaves * 64) attend_kernel(Args a) {
                 for (int j = 0; j < W; ++j) o[u][j] *= f;
         }
         const float base = m == -INFINITY ? 0.0f : m;
-        float p[8];
+        float p[H * 4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < H * 4; ++i) {
             p[i] = __builtin_amdgcn_exp2f(s[i / 4][i % 4] - base);
             l += p[i];
             if constexpr (I8) p[i] *= vs[i / 4][i % 4];
         }
         if (!whole) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < H * 4; ++i)
                 if (!use[i / 4][i % 4]) {
                     p[i] = 0.0f;                       // (the scale may be anything)
 #pragma unroll
                     for (int u = 0; u < NU; ++u) vreg[i][u] = u4{0, 0, 0, 0};
                 }
         }
-        u4 pp[PP];
+        // two blocks are the 32 tokens of a product
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t x[PP];
-            split2<PP>(p[2 * i], p[2 * i + 1], x);
+        for (int y2 = 0; y2 < H / 2; ++y2) {
+            u4 pp[PP];
 #pragma unroll
-            for (int n = 0; n < PP; ++n) pp[n][i] = x[n];
-        }
+            for (int i = 0; i < 4; ++i) {
+                uint32_t x[PP];
+                split2<PP>(p[8 * y2 + 2 * i], p[8 * y2 + 2 * i + 1], x);
 #pragma unroll
-        for (int u = 0; u < NU; ++u) {
-            u4 v[8];
+                for (int n = 0; n < PP; ++n) pp[n][i] = x[n];
+            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if constexpr (!I8) v[i] = vreg[i][u];
-                else if constexpr (W == 8) v[i] = widen8(u2{vreg[i][u][0], vreg[i][u][1]});
-                else {
-                    const u2 x = widen4(vreg[i][u][0]);
-                    v[i] = u4{x[0], x[1], 0, 0};
+            for (int u = 0; u < NU; ++u) {
+                if constexpr (!I8) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) {
+                        u4 t;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            t[i] = __builtin_amdgcn_perm(vreg[8 * y2 + 2 * i + 1][u][j / 2], vreg[8 * y2 + 2 * i][u][j / 2], j & 1 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+                        for (int n = 0; n < PP; ++n) o[u][j] = mfma(t, pp[n], o[u][j]);
+                    }
+                } else {
+                    // four d at a time: the 4 x 4 bytes of four tokens turned, then
+                    // widened, are the operand's two dwords of those tokens
+#pragma unroll
+                    for (int c = 0; c < W / 4; ++c) {
+                        uint32_t t[2][4];
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const int at = 8 * y2 + 4 * hf;
+                            turn4(vreg[at][u][c], vreg[at + 1][u][c], vreg[at + 2][u][c], vreg[at + 3][u][c], t[hf]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const u2 x = widen4(t[0][j]), y = widen4(t[1][j]);
+#pragma unroll
+                            for (int n = 0; n < PP; ++n) o[u][4 * c + j] = mfma(u4{x[0], x[1], y[0], y[1]}, pp[n], o[u][4 * c + j]);
+                        }
+                    }
                 }
             }
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                u4 t;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    t[i] = __builtin_amdgcn_perm(v[2 * i + 1][j / 2], v[2 * i][j / 2], j & 1 ? 0x07060302u : 0x05040100u);
-#pragma unroll
-                for (int n = 0; n < PP; ++n) o[u][j] = mfma(t, pp[n], o[u][j]);
-            }
         }
-        (void)v_ok;
         if (more) load_v(step + 1);
     }
 
@@ -356,150 +477,213 @@ __global__ void __launch_bounds__(kWaves * 64) attend_kernel(Args a) {
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) M = fmaxf(M, s_m[w][col]);
     const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - M);
+    if (col < heads)
 #pragma unroll
-    for (int u = 0; u < NU; ++u)
+        for (int u = 0; u < NU; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < W; ++j) s_o[wave][col][W * (4 * g4 + i) + 16 * W * u + j] = o[u][j][i] * f;
+                for (int j = 0; j < W; j += 4)
+                    *reinterpret_cast<f4 *>(&s_o[wave][col][W * (4 * g4 + i) + 16 * W * u + j]) =
+                        f4{o[u][j][i], o[u][j + 1][i], o[u][j + 2][i], o[u][j + 3][i]} * f;
     __syncthreads();
-    for (int x = threadIdx.x; x < heads * (D / 4); x += kWaves * 64) {
+    for (int x = threadIdx.x; x < heads * (D / 4); x += kThreads) {
         const int g = x / (D / 4), d = (x - g * (D / 4)) * 4;
-        f4 r = {0, 0, 0, 0};
+        f4 r4 = {0, 0, 0, 0};
         float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, s_m[w][g]);
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            const float *po = &s_o[w][g][d];
-            r += f4{po[0], po[1], po[2], po[3]};
+            r4 += *reinterpret_cast<const f4 *>(&s_o[w][g][d]);
             if (s_m[w][g] != -INFINITY) ll += s_l[w][g] * __builtin_amdgcn_exp2f(s_m[w][g] - mm);
         }
-        if (a.splits > 1) {
-            *reinterpret_cast<f4 *>(a.part + ((head0 + g) * a.splits + sp) * D + d) = r;
+        if constexpr (!DIRECT) {
+            const int64_t part = (blockIdx.x + (int64_t)b * rows_of_seq + r) * a.tile_heads + g;
+            *reinterpret_cast<f4 *>(a.part + part * D + d) = r4;
             if (d == 0) {
-                float *st = a.stat + ((head0 + g) * a.splits + sp) * 2;
-                st[0] = mm;
-                st[1] = ll;
+                a.stat[part * 2] = mm;
+                a.stat[part * 2 + 1] = ll;
             }
         } else {
             const float inv = mm == -INFINITY ? 0.0f : 1.0f / ll;
             const int64_t at = (int64_t)b * a.out_ld + (int64_t)(h * a.G + g0 + g) * D + d;
-            if constexpr (BF16)
-                *reinterpret_cast<u2 *>(static_cast<uint16_t *>(a.out) + at) = u2{pack2(r[0] * inv, r[1] * inv), pack2(r[2] * inv, r[3] * inv)};
-            else
-                *reinterpret_cast<f4 *>(static_cast<float *>(a.out) + at) = r * inv;
-            if (d == 0) {
-                if (a.lse) a.lse[head0 + g] = mm == -INFINITY ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
-                if (TRACK) {
-                    a.stat[(head0 + g) * 2] = mm;
-                    a.stat[(head0 + g) * 2 + 1] = ll;
-                }
-            }
+            store4<BF16>(a.out, at, r4 * inv);
+            if (d == 0 && a.lse) a.lse[head0 + g] = mm == -INFINITY ? -INFINITY : (mm + log2f(ll)) * kLn2;
         }
+    }
+    if constexpr (DIRECT) return;
+    u += here;
+    if (u >= u_end) return;
+    // the next row with tokens
+    step0 = 0;
+    if (++r == rows_of_seq) {
+        r = 0;
+        do len = length_of(a, ++b); while (len == 0);   // (u < u_end: there is one)
+    }
+    __syncthreads();
     }
 }
 
-// Statistics of a head over its chunks, by one wave: all lanes get the maximum
+// Statistics of a head over its n parts, by one wave: all lanes get the maximum
 // and the sum relative to it.
-__device__ __forceinline__ void join_stats(const float *st, int n, int lane, float &M, float &L) {
+__device__ __forceinline__ void join_stats(const float *st, int n, int stride, int lane, float &M, float &L) {
     M = -INFINITY;
-    for (int i = lane; i < n; i += 64) M = fmaxf(M, st[2 * i]);
+    for (int i = lane; i < n; i += 64) M = fmaxf(M, st[(int64_t)i * stride]);
     for (int o = 1; o < 64; o *= 2) M = fmaxf(M, __shfl_xor(M, o));
     L = 0.0f;
     for (int i = lane; i < n; i += 64)
-        if (st[2 * i] != -INFINITY) L += st[2 * i + 1] * __builtin_amdgcn_exp2f(st[2 * i] - M);
+        if (st[(int64_t)i * stride] != -INFINITY) L += st[(int64_t)i * stride + 1] * __builtin_amdgcn_exp2f(st[(int64_t)i * stride] - M);
     for (int o = 1; o < 64; o *= 2) L += __shfl_xor(L, o);
 }
 
-// Joins the chunks: block x < q heads writes the output of head x; the others
-// add the weights of 1024 slots of one key-value head.
-template <bool BF16>
-__global__ void __launch_bounds__(256) join_kernel(Args a) {
-    __shared__ float s_o[4][256];
+constexpr int kJoin = 256;     // threads of a joining workgroup
+
+// Joins the parts of rows.  The first outs workgroups write outputs, a head by
+// TPH threads each (all of a workgroup where heads are few, a wave where there
+// are many); the others add the weights of kJoin * 4 slots of one key-value
+// head.  All parts' factors come first, so that the loads of the partial outputs
+// depend on nothing and are in flight together: everything comes from the
+// caches, and latency is all there is.
+template <bool BF16, int TPH>
+__global__ void __launch_bounds__(kJoin) join_kernel(Args a, int outs) {
+    constexpr int HEADS = kJoin / TPH;
+    __shared__ float s_o[kJoin][4];
+    __shared__ float s_f[HEADS][TPH == 64 ? 1 : kMaxGroups];
     __shared__ float s_m[64], s_i[64];
-    const int b = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, D = a.c.D;
-    const int len = min(max(a.lens[b], 0), a.max_len);
-    const int n = min(a.splits, (len + a.chunk - 1) / a.chunk);
-    const int outs = a.splits > 1 ? a.hq : 0;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, D = a.c.D;
+    const int rows_of_seq = a.c.heads * a.tiles;
+    const int64_t per = a.first[a.c.batch];
+    // parts of head g of key-value head h of sequence b: their number, and the first
+    auto parts = [&](int b, int steps, int h, int g, int64_t &part) {
+        const int r = h * a.tiles + g / 16;
+        const int64_t u = a.first[b] * rows_of_seq + (int64_t)r * steps, w0 = u / per;
+        part = (w0 + (int64_t)b * rows_of_seq + r) * a.tile_heads + g % 16;
+        return steps ? (int)((u + steps - 1) / per - w0) + 1 : 0;
+    };
     if ((int)blockIdx.x < outs) {
-        const int i = blockIdx.x;
-        const int64_t head = (int64_t)b * a.hq + i;
-        const float *st = a.stat + head * a.splits * 2;
+        const int64_t head = (int64_t)blockIdx.x * HEADS + threadIdx.x / TPH;
+        if (head >= (int64_t)a.c.batch * a.hq) return;   // (whole waves; with TPH = kJoin none)
+        const int b = (int)(head / a.hq), i = (int)(head - (int64_t)b * a.hq), t = threadIdx.x % TPH;
+        int64_t part;
+        const int n = parts(b, steps_of(a, length_of(a, b)), i / a.G, i % a.G, part);
+        const float *st = a.stat + part * 2, *po = a.part + part * D;
+        const int stride = a.tile_heads * 2;
         float M, L;
-        join_stats(st, n, lane, M, L);
+        join_stats(st, n, stride, lane, M, L);
+        auto factor = [&](int s) {
+            const float m = st[(int64_t)s * stride];
+            return m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - M);
+        };
         f4 r = {0, 0, 0, 0};
-        if (lane * 4 < D)
-            for (int s = wave; s < n; s += 4) {
-                const float m = st[2 * s];
-                if (m == -INFINITY) continue;
-                r += *reinterpret_cast<const f4 *>(a.part + (head * a.splits + s) * D + lane * 4) * __builtin_amdgcn_exp2f(m - M);
-            }
-        *reinterpret_cast<f4 *>(&s_o[wave][lane * 4]) = r;
-        __syncthreads();
-        if (wave == 0 && lane * 4 < D) {
+        const int quads = D / 4;
+        if constexpr (TPH == 64) {
+            if (t < quads)
+#pragma unroll 4
+                for (int s = 0; s < n; ++s) r += *reinterpret_cast<const f4 *>(po + (int64_t)s * a.tile_heads * D + t * 4) * factor(s);
+        } else {
+            for (int s = t; s < n; s += TPH) s_f[0][s] = factor(s);
+            __syncthreads();
+            const int groups = TPH / quads, group = t / quads, d = (t - group * quads) * 4;
+            if (group < groups)
+#pragma unroll 8
+                for (int s = group; s < n; s += groups) r += *reinterpret_cast<const f4 *>(po + (int64_t)s * a.tile_heads * D + d) * s_f[0][s];
+            *reinterpret_cast<f4 *>(s_o[t]) = r;
+            __syncthreads();
+            if (t < quads)
+                for (int g = 1; g < min(groups, n); ++g) r += *reinterpret_cast<const f4 *>(s_o[t + g * quads]);
+        }
+        if (t < quads) {
             const float inv = M == -INFINITY ? 0.0f : 1.0f / L;
-            for (int w = 1; w < 4; ++w) r += *reinterpret_cast<const f4 *>(&s_o[w][lane * 4]);
-            const int64_t at = (int64_t)b * a.out_ld + (int64_t)i * D + lane * 4;
-            if constexpr (BF16)
-                *reinterpret_cast<u2 *>(static_cast<uint16_t *>(a.out) + at) = u2{pack2(r[0] * inv, r[1] * inv), pack2(r[2] * inv, r[3] * inv)};
-            else
-                *reinterpret_cast<f4 *>(static_cast<float *>(a.out) + at) = r * inv;
-            if (lane == 0 && a.lse) a.lse[head] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+            store4<BF16>(a.out, (int64_t)b * a.out_ld + (int64_t)i * D + t * 4, r * inv);
+            if (t == 0 && a.lse) a.lse[head] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * kLn2;
         }
         return;
     }
-    const int blocks = (a.max_len + 1023) / 1024;
-    const int x = blockIdx.x - outs, h = x / blocks, j = (x - h * blocks) * 1024 + threadIdx.x * 4;
-    if ((x - h * blocks) * 1024 >= len) return;
-    const int64_t head0 = (int64_t)b * a.hq + (int64_t)h * a.G;
-    f4 w = {0, 0, 0, 0};
+    const int blocks = (a.max_len + kJoin * 4 - 1) / (kJoin * 4);
+    const int64_t id = blockIdx.x - outs;
+    const int row = (int)(id / blocks), b = row / a.c.heads, h = row - b * a.c.heads;
+    const int j0 = (int)(id - (int64_t)row * blocks) * kJoin * 4, j = j0 + threadIdx.x * 4;
+    const int len = length_of(a, b);
+    if (j0 >= len) return;
+    const int64_t at = (int64_t)row * a.c.slots() + j;
+    auto scores = [&](int g) {
+        return *reinterpret_cast<const f4 *>(a.scores + (((int64_t)row * a.tiles + g / 16) * a.score_ld + (j & ~15)) * a.tile_heads + (g % 16) * 16 + (j & 15));
+    };
+    // scores and weights are asked for before the statistics are waited for
+    constexpr int AHEAD = 8;
+    f4 ahead[AHEAD], w = {0, 0, 0, 0};
+    if (j < len) {
+#pragma unroll
+        for (int g = 0; g < AHEAD; ++g)
+            if (g < a.G) ahead[g] = scores(g);
+        w = *reinterpret_cast<const f4 *>(a.weight + at);   // (slots come in whole pages)
+    }
+    f4 add = {0, 0, 0, 0};
     for (int g0 = 0; g0 < a.G; g0 += 64) {
         const int gn = min(64, a.G - g0);
-        __syncthreads();
-        for (int g = wave; g < gn; g += 4) {
+        if (g0) __syncthreads();
+        for (int g = wave; g < gn; g += kJoin / 64) {
+            int64_t part;
+            const int n = parts(b, steps_of(a, len), h, g0 + g, part);
             float M, L;
-            join_stats(a.stat + (head0 + g0 + g) * a.splits * 2, n, lane, M, L);
+            join_stats(a.stat + part * 2, n, a.tile_heads * 2, lane, M, L);
             if (lane == 0) {
                 s_m[g] = M == -INFINITY ? 0.0f : M;
                 s_i[g] = M == -INFINITY ? 0.0f : 1.0f / L;
             }
         }
         __syncthreads();
-        if (j < len)
-            for (int g = 0; g < gn; ++g) {
-                const f4 s = *reinterpret_cast<const f4 *>(a.scores + (head0 + g0 + g) * a.score_ld + j);
+        auto take = [&](const f4 &s, int g) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] += __builtin_amdgcn_exp2f(s[e] - s_m[g]) * s_i[g];
+            for (int e = 0; e < 4; ++e) add[e] += __builtin_amdgcn_exp2f(s[e] - s_m[g]) * s_i[g];
+        };
+        if (j < len) {
+            if (g0 == 0) {
+#pragma unroll
+                for (int g = 0; g < AHEAD; ++g)
+                    if (g < gn) take(ahead[g], g);
             }
+            for (int g = g0 == 0 ? AHEAD : 0; g < gn; ++g)
+                take(scores(g0 + g), g);
+        }
     }
-    const int64_t at = ((int64_t)b * a.c.heads + h) * a.c.slots() + j;
-    for (int e = 0; e < 4; ++e)
-        if (j + e < len) a.weight_out[at + e] = a.weight[at + e] + w[e];
+    w += add;
+    if (j + 4 <= len) *reinterpret_cast<f4 *>(a.weight_out + at) = w;
+    else
+        for (int e = 0; e < 4; ++e)
+            if (j + e < len) a.weight_out[at + e] = w[e];
 }
 
-// Chunks of a call: enough workgroups for the device, but not shorter than one
-// step of every wave.
+// How a call is run.  Direct up to kDirect tokens: a workgroup walks them in
+// fewer microseconds than the joining kernel costs.
+constexpr int kDirect = 512;
+// Shares per CU otherwise: what is resident at once of the commonest variant
+// (2 and 4 were within 3% for 131071 tokens and for batches).
+constexpr int kGroupsPerCu = 3;
 struct Plan {
-    int chunk, splits, score_ld;
-    size_t part, stat, scores;   // bytes
+    bool direct;
+    int tiles, tile_heads, groups, score_ld;
+    size_t part, stat, first, scores;   // bytes
 };
 Plan plan_of(const rq_kv_cache *c, int q_heads, int64_t max_len, int track) {
-    Plan p;
+    Plan p{};
     const int G = q_heads / c->heads;
-    const int64_t rows = (int64_t)c->batch * c->heads * ((G + 15) / 16);
-    const int64_t step = kWaves * kTile;
-    const int64_t want = std::max<int64_t>(1, (4 * (int64_t)device_cus() + rows - 1) / std::max<int64_t>(rows, 1));
-    int64_t chunk = (max_len + want - 1) / want;
-    chunk = std::max(step, (chunk + step - 1) / step * step);
-    p.chunk = (int)chunk;
-    p.splits = (int)std::max<int64_t>(1, (max_len + chunk - 1) / chunk);
-    p.score_ld = (int)((max_len + kTile - 1) / kTile * kTile);
-    const size_t heads = (size_t)c->batch * q_heads;
+    p.tiles = (G + 15) / 16;
+    p.tile_heads = std::min(G, 16);
+    p.direct = !track && max_len <= kDirect && (int64_t)c->batch * c->heads * p.tiles <= (1 << 20);
+    p.score_ld = (int)((max_len + 63) / 64 * 64);   // whole steps of a wave are written
+    if (p.direct) return p;
+    const int64_t rows = (int64_t)c->batch * c->heads * p.tiles;
+    // (the least step, whatever the type of the queries: the workspace does not depend on it)
+    const int64_t steps = rows * ((max_len + kLeastStep - 1) / kLeastStep);
+    p.groups = (int)std::max<int64_t>(1, std::min<int64_t>({steps, (int64_t)device_cus() * kGroupsPerCu, kMaxGroups}));
     auto round = [](size_t n) { return (n + 15) / 16 * 16; };
-    p.part = p.splits > 1 ? round(heads * p.splits * c->head_dim * 4) : 0;
-    p.stat = p.splits > 1 || track ? round(heads * p.splits * 8) : 0;
-    p.scores = track ? round(heads * p.score_ld * 4) : 0;
+    const size_t parts = (size_t)(p.groups + rows) * p.tile_heads;
+    p.part = round(parts * c->head_dim * 4);
+    p.stat = round(parts * 8);
+    p.first = round(((size_t)c->batch + 1) * 8);
+    p.scores = track ? round((size_t)rows * p.tile_heads * p.score_ld * 4) : 0;
     return p;
 }
 
@@ -507,7 +691,7 @@ Plan plan_of(const rq_kv_cache *c, int q_heads, int64_t max_len, int track) {
 
 size_t attend_workspace_bytes(const rq_kv_cache *c, int q_heads, int64_t max_len, int track) {
     const Plan p = plan_of(c, q_heads, max_len, track);
-    return p.part + p.stat + p.scores;
+    return p.part + p.stat + p.first + p.scores;
 }
 
 int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_t q_ld, int q_heads,
@@ -522,23 +706,27 @@ int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_
     char *ws = static_cast<char *>(workspace);
     a.part = reinterpret_cast<float *>(ws);
     a.stat = reinterpret_cast<float *>(ws + p.part);
-    a.scores = reinterpret_cast<float *>(ws + p.part + p.stat);
+    a.first = reinterpret_cast<int64_t *>(ws + p.part + p.stat);
+    a.scores = reinterpret_cast<float *>(ws + p.part + p.stat + p.first);
     a.q_ld = q_ld, a.out_ld = out_ld, a.mask_ld = mask_ld;
-    a.hq = q_heads, a.G = q_heads / c->heads, a.max_len = (int)max_len;
-    a.chunk = p.chunk, a.splits = p.splits, a.score_ld = p.score_ld;
+    a.hq = q_heads, a.G = q_heads / c->heads, a.tiles = p.tiles, a.tile_heads = p.tile_heads;
+    a.max_len = (int)max_len, a.score_ld = p.score_ld, a.step_log = ilog2(step_of(c->head_dim > 128 ? 256 : c->head_dim > 64 ? 128 : 64, c->dtype == RQ_I8, bf16));
     a.scale2 = scale * 1.4426950408889634f;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const dim3 grid(p.splits, c->heads * ((a.G + 15) / 16), c->batch);
-    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(kWaves * 64), 0, s, a); };
+    const unsigned groups = p.direct ? (unsigned)c->batch * c->heads * p.tiles : (unsigned)p.groups;
+    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(groups), dim3(kThreads), 0, s, a); };
     auto pick = [&](auto dp, auto exact, auto i8, auto io) {
         constexpr int DP = decltype(dp)::value;
         constexpr bool E = decltype(exact)::value, I = decltype(i8)::value, B = decltype(io)::value;
-        if (mask) {
-            if (track) go(attend_kernel<DP, E, I, B, true, true>);
-            else go(attend_kernel<DP, E, I, B, true, false>);
+        if (p.direct) {
+            if (mask) go(attend_kernel<DP, E, I, B, true, false, true>);
+            else go(attend_kernel<DP, E, I, B, false, false, true>);
+        } else if (mask) {
+            if (track) go(attend_kernel<DP, E, I, B, true, true, false>);
+            else go(attend_kernel<DP, E, I, B, true, false, false>);
         } else {
-            if (track) go(attend_kernel<DP, E, I, B, false, true>);
-            else go(attend_kernel<DP, E, I, B, false, false>);
+            if (track) go(attend_kernel<DP, E, I, B, false, true, false>);
+            else go(attend_kernel<DP, E, I, B, false, false, false>);
         }
     };
     auto types = [&](auto dp, auto exact) {
@@ -555,12 +743,17 @@ int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_
     if (c->head_dim <= 64) dims(std::integral_constant<int, 64>{});
     else if (c->head_dim <= 128) dims(std::integral_constant<int, 128>{});
     else dims(std::integral_constant<int, 256>{});
-    const int weights = track ? (int)((max_len + 1023) / 1024) * c->heads : 0;
-    const int outs = p.splits > 1 ? q_heads : 0;
-    if (outs + weights > 0) {
-        const dim3 jg(outs + weights, c->batch);
-        if (bf16) hipLaunchKernelGGL(join_kernel<true>, jg, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL(join_kernel<false>, jg, dim3(256), 0, s, a);
+    if (!p.direct) {
+        const int64_t heads = (int64_t)c->batch * q_heads;
+        const int64_t weights = track ? (max_len + kJoin * 4 - 1) / (kJoin * 4) * c->batch * c->heads : 0;
+        // a wave a head once that fills the device
+        const bool many = heads >= 4 * device_cus();
+        const int64_t outs = many ? (heads + kJoin / 64 - 1) / (kJoin / 64) : heads;
+        // (workgroups of 256: a launch holds 2^24 of them)
+        if (outs + weights >= (1 << 24)) return (int)hipErrorInvalidValue;
+        auto join = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((unsigned)(outs + weights)), dim3(kJoin), 0, s, a, (int)outs); };
+        if (bf16) many ? join(join_kernel<true, 64>) : join(join_kernel<true, kJoin>);
+        else many ? join(join_kernel<false, 64>) : join(join_kernel<false, kJoin>);
     }
     return (int)hipGetLastError();
 }
