@@ -119,20 +119,37 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(Args a) {
     const int half = a.rot / 2;
     const int ia = !INTER && turned ? item * 4 : item * 8, ib = !INTER && turned ? ia + half : ia + 4;
 
+    // (visits may touch any memory, so the weights are read before them)
     float wq[8], wk[8];
+    const f4 one = {1, 1, 1, 1};
+    const int da = live ? ia : 0, db = live ? ib : 0;
+    const f4 q0 = a.qw ? *reinterpret_cast<const f4 *>(a.qw + da) : one, q1 = a.qw ? *reinterpret_cast<const f4 *>(a.qw + db) : one;
+    const f4 k0 = a.kw ? *reinterpret_cast<const f4 *>(a.kw + da) : one, k1 = a.kw ? *reinterpret_cast<const f4 *>(a.kw + db) : one;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int d = (i < 4 ? ia : ib - 4) + i;
-        wq[i] = live && a.qw ? a.qw[d] : 1.0f;
-        wk[i] = live && a.kw ? a.kw[d] : 1.0f;
-    }
+    for (int i = 0; i < 4; ++i) wq[i] = q0[i], wq[4 + i] = q1[i], wk[i] = k0[i], wk[4 + i] = k1[i];
     const float inv_d = 1.0f / (float)D;
     const int64_t visits = a.T * a.chunks, stride = (int64_t)gridDim.x * 4;
     for (int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); id < visits; id += stride) {
         const int64_t t = a.chunks == 1 ? id : id / a.chunks;
         const int first = a.chunks == 1 ? 0 : (int)(id - t * a.chunks) * a.per * HPW;
         const int last = min(a.nh, first + a.per * HPW);
+        Raw<BF16> raw[U];
+        auto load = [&](int h0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int h = h0 + u * HPW;
+                if (live && h < last) {
+                    const int64_t in = t * a.ld + (int64_t)h * D;
+                    raw[u] = load8<BF16, INTER>(a.qkv, in + ia, in + ib);
+                } else raw[u] = {};
+            }
+        };
+        // The heads are asked for before anything is waited for, then the three
+        // numbers of the token, then what depends on them.
+        load(first + slot);
         const int64_t p = a.positions ? a.positions[t] : t;
+        const int64_t b = a.c.k && a.seq ? a.seq[t] : t;
+        const int32_t place = a.c.k ? a.place[t] : -1;
         float c[4] = {1, 1, 1, 1}, s[4] = {0, 0, 0, 0};
         if (turned) {
             const bool in_table = p >= 0 && p < a.table_rows;
@@ -147,24 +164,12 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(Args a) {
         // the row of the cache that head 0 goes to, -1: none
         int64_t row0 = -1, meta = 0;
         const int page = 1 << a.c.page_log;
-        if (a.c.k) {
-            const int64_t b = a.seq ? a.seq[t] : t;
-            const int32_t place = a.place[t];
-            if (b >= 0 && b < a.c.batch && place >= 0 && place < a.c.slots()) {
-                row0 = a.c.row((int)b, 0, place);
-                meta = b * a.hkv * a.c.slots() + place;
-            }
+        if (b >= 0 && b < a.c.batch && place >= 0 && place < a.c.slots()) {
+            row0 = a.c.row((int)b, 0, place);
+            meta = b * a.hkv * a.c.slots() + place;
         }
         for (int h0 = first + slot; h0 - slot < last; h0 += HPW * U) {
-            Raw<BF16> raw[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = h0 + u * HPW;
-                if (live && h < last) {
-                    const int64_t in = t * a.ld + (int64_t)h * D;
-                    raw[u] = load8<BF16, INTER>(a.qkv, in + ia, in + ib);
-                } else raw[u] = {};
-            }
+            if (h0 != first + slot) load(h0);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int h = h0 + u * HPW;
@@ -259,7 +264,9 @@ int launch_qk_norm_rope(const rq_qk_norm *d, const void *qkv, int bf16, int64_t 
     const int64_t full = (int64_t)device_cus() * 32;
     a.per = (int)std::min<int64_t>(groups, std::max<int64_t>(1, T * groups / full));
     a.chunks = (groups + a.per - 1) / a.per;
-    const int64_t wgs = std::min<int64_t>((T * a.chunks + 3) / 4, int64_t(1) << 20);
+    // Twice what is resident, then waves walk over visits: 32760 tokens of 24 heads
+    // take 87 us, one visit a wave 101 us, a single round of waves 91 us.
+    const int64_t wgs = std::min<int64_t>((T * a.chunks + 3) / 4, (int64_t)device_cus() * 8);
     auto go = [&](auto kern) {
         hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(256), 0, static_cast<hipStream_t>(stream), a);
     };
