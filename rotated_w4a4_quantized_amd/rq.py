@@ -169,7 +169,9 @@ def _t_ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        # (the address alone: torch.cuda.current_stream() builds a Stream object
+        # around it, which costs as much as a launch)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -550,13 +552,15 @@ def _vector(t, n, dtype, name):
     return t.data_ptr()
 
 
-def _on_device(device, **tensors):
+def _on_device(index, *tensors):
+    """Refuse buffers that are not all on the current GPU (index: the first
+    one's get_device(), -1 for host memory)."""
     import torch
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"the buffers are on {device}, which is not the current GPU")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if index < 0 or index != torch.cuda.current_device():
+        raise ValueError(f"the buffers are on device {index}, which is not the current GPU")
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"a buffer is on device {t.get_device()}, not on {index}")
 
 
 class KVCache:
@@ -586,7 +590,6 @@ class KVCache:
         self.weight, self.pos = weight, pos
         self.heads, self.head_dim, self.page, self.batch = heads, D, page, table.shape[0]
         self.slots = table.shape[1] * page
-        self.device = k.device
         for name, t in (("v", v), ("table", table), ("k_scale", k_scale), ("v_scale", v_scale),
                         ("weight", weight), ("pos", pos)):
             if t is not None and t.device != k.device:
@@ -651,8 +654,8 @@ def qk_norm_rope(norm: QKNorm, qkv, q_out, k_out=None, positions=None, cache: KV
     if q_out.dtype is not qkv.dtype or (k_out is not None and k_out.dtype is not qkv.dtype):
         raise TypeError("q_out and k_out must have qkv's type")
     qw, kw = norm.q_heads * D, norm.kv_heads * D
-    _on_device(qkv.device, q_out=q_out, k_out=k_out, positions=positions, seq=seq, place=place,
-               cache=cache, cos=norm.cos)
+    _on_device(qkv.get_device(), q_out, k_out, positions, seq, place, norm.cos, norm.q_weight,
+               norm.k_weight, None if cache is None else cache.k)
     p_in, ld = _rows(qkv, T, qw + kw * (1 if cache is None else 2), "qkv")
     p_q, q_ld = _rows(q_out, T, qw, "q_out")
     p_k, k_ld = (None, 0) if k_out is None else _rows(k_out, T, kw, "k_out")
@@ -685,8 +688,7 @@ def paged_attention(q, cache: KVCache, lens, out, scale=None, max_len=None, mask
     width = q.shape[1] if q.dim() == 2 else q.shape[1] * q.shape[2]
     if width % D:
         raise ValueError(f"a row of q must be whole heads of {D}, got {width}")
-    _on_device(q.device, cache=cache, lens=lens, out=out, mask=mask, lse=lse,
-               weight_out=weight_out, workspace=workspace)
+    _on_device(q.get_device(), cache.k, lens, out, mask, lse, weight_out, workspace)
     p_q, q_ld = _rows(q, B, width, "q")
     p_o, o_ld = _rows(out, B, width, "out")
     if max_len is None:
@@ -724,8 +726,7 @@ def cache_evict(cache: KVCache, lens, keep, recent=0, sink=0, max_len=None, lens
     B = cache.batch
     if cache.weight is None or cache.pos is None:
         raise ValueError("eviction needs a cache with weight and pos")
-    _on_device(cache.device, lens=lens, lens_out=lens_out, weight_out=weight_out, pos_out=pos_out,
-               workspace=workspace)
+    _on_device(cache.k.get_device(), lens, lens_out, weight_out, pos_out, workspace)
     n = B * cache.heads * cache.slots
     p_lens = _vector(lens, B, torch.int32, "lens")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
