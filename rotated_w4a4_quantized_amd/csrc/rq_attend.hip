@@ -44,16 +44,17 @@ struct Args {
     float scale2;    // scale * log2(e)
 };
 
-constexpr int kWaves = 4;      // waves of a workgroup
+// Waves of a workgroup: 4, and 8 in a direct call, which has one workgroup a row
+// and wants it done soon.
+constexpr int waves_of(bool direct) { return direct ? 8 : 4; }
 // 16-token blocks of one wave's step: 16 KB of keys and values of 128 dimensions
 // are in flight per wave for either type.  (int8 steps of 2 blocks took 5% longer
 // on 48 sequences of 4096 tokens; fp32 queries and D > 128 leave no registers for
 // 4.)
 constexpr int blocks_of(int DP, bool i8, bool bf16) { return i8 && bf16 && DP <= 128 ? 4 : 2; }
 // tokens of one workgroup's step
-constexpr int step_of(int DP, bool i8, bool bf16) { return kWaves * 16 * blocks_of(DP, i8, bf16); }
-constexpr int kLeastStep = kWaves * 32;
-constexpr int kThreads = kWaves * 64;
+constexpr int step_of(int DP, bool i8, bool bf16, bool direct) { return waves_of(direct) * 16 * blocks_of(DP, i8, bf16); }
+constexpr int kLeastStep = waves_of(false) * 32;
 constexpr int kMaxGroups = 1024;   // workgroups of a divided call, at most
 
 // waves of a SIMD, by the registers they need
@@ -139,12 +140,13 @@ __device__ __forceinline__ int steps_of(const Args &a, int len) { return (int)((
 // and three for fp32: with one part their rounding would be as large as the
 // output's own.  Sums and statistics are fp32.
 template <int DP, bool EXACT, bool I8, bool BF16, bool MASKED, bool TRACK, bool DIRECT>
-__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(resident(DP, EXACT, BF16, I8)))) attend_kernel(Args a) {
+__global__ void __launch_bounds__(waves_of(DIRECT) * 64) __attribute__((amdgpu_waves_per_eu(DIRECT ? 1 : resident(DP, EXACT, BF16, I8)))) attend_kernel(Args a) {
     constexpr int QP = BF16 ? 1 : 3, PP = BF16 ? 2 : 3;
     constexpr int KS = DP / 32;                  // products along d
     constexpr int W = DP == 64 ? 4 : 8;          // d of one value load
     constexpr int NU = DP / (16 * W);            // value loads of a token
-    constexpr int H = blocks_of(DP, I8, BF16), TILE = 16 * H, STEP = step_of(DP, I8, BF16);
+    constexpr int H = blocks_of(DP, I8, BF16), TILE = 16 * H, STEP = step_of(DP, I8, BF16, DIRECT);
+    constexpr int kWaves = waves_of(DIRECT), kThreads = kWaves * 64;
     __shared__ float s_m[kWaves][16], s_l[kWaves][16];
     __shared__ float s_o[kWaves][16][DP + 4];
 
@@ -213,13 +215,22 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(r
         step0 = __builtin_amdgcn_readfirstlane((int)(off - (int64_t)r * n));
     }
 
-    for (;;) {
+    for (;;) {   // (rows of this workgroup; the body keeps its indentation)
     const int row_steps = steps_of(a, len);
     const int here = DIRECT ? row_steps : (int)min((int64_t)(row_steps - step0), u_end - u);
     const int begin = step0 * STEP, end = min(len, begin + here * STEP);
     const int h = r / a.tiles, g0 = (r - h * a.tiles) * 16;
     const int heads = min(16, a.G - g0);
     const int64_t head0 = (int64_t)b * a.hq + h * a.G + g0;
+
+    // the pages of this wave's next 64 / H steps: lane H i + block
+    int32_t page_of = -1;
+    auto load_pages = [&](int step) {
+        const int j = begin + ((step + lane / H) * kWaves + wave) * TILE + (lane % H) * 16;
+        const int idx = j >> a.c.page_log;   // (asked for without waiting for the length)
+        page_of = idx < a.c.table_ld ? a.c.table[(int64_t)b * a.c.table_ld + idx] : -1;
+    };
+    load_pages(0);
 
     // queries: piece s of lane (head, g4) holds d_of(s) .. + 7
     auto d_of = [&](int s) { return I8 && EXACT ? (s >> 1) * 64 + g4 * 16 + (s & 1) * 8 : s * 32 + g4 * 8; };
@@ -258,17 +269,11 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(r
     const int steps = here;
     const int page_mask = (1 << a.c.page_log) - 1;
 
-    // the pages of this wave's next 64 / H steps: lane H i + block
-    int32_t page_of = -1;
-    auto load_pages = [&](int step) {
-        const int j = begin + ((step + lane / H) * kWaves + wave) * TILE + (lane % H) * 16;
-        page_of = j < end ? a.c.table[(int64_t)b * a.c.table_ld + (j >> a.c.page_log)] : -1;
-    };
     // base row of block x of a step; `there`: whether it has a page
     auto row_of = [&](int step, int x, bool &there) -> int64_t {
         const int j = begin + (step * kWaves + wave) * TILE + x * 16;
         const int32_t pg = __builtin_amdgcn_readlane(page_of, (step & (64 / H - 1)) * H + x);
-        there = (uint32_t)pg < (uint32_t)a.c.pages;
+        there = (uint32_t)pg < (uint32_t)a.c.pages && j < end;
         return (((int64_t)(there ? pg : 0) * a.c.heads + h) << a.c.page_log) + (j & page_mask);
     };
 
@@ -328,7 +333,6 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(r
 
     auto mine = [&](int step) { return begin + (step * kWaves + wave) * TILE < end; };   // wave-uniform
     if (mine(0)) {
-        load_pages(0);
         load_k(0);
         load_v(0);
     }
@@ -656,7 +660,11 @@ __global__ void __launch_bounds__(kJoin) join_kernel(Args a, int outs) {
 }
 
 // How a call is run.  Direct up to kDirect tokens: a workgroup walks them in
-// fewer microseconds than the joining kernel costs.
+// fewer microseconds than the joining kernel costs (8 sequences of 512 tokens: 9.4
+// us against 14.3).  Direct too where the rows fill the device and are many for
+// their length, so that uneven ones even out: 256 sequences of 2000 tokens, 8 heads
+// 350 us (6.0 TB/s) against 376, uneven 195 against 217; 128 of 4000, uneven 204
+// against 203; but 64 of up to 8000, uneven 221 against 197.
 constexpr int kDirect = 512;
 // Shares per CU otherwise: what is resident at once of the commonest variant
 // (2 and 4 were within 3% for 131071 tokens and for batches).
@@ -671,10 +679,10 @@ Plan plan_of(const rq_kv_cache *c, int q_heads, int64_t max_len, int track) {
     const int G = q_heads / c->heads;
     p.tiles = (G + 15) / 16;
     p.tile_heads = std::min(G, 16);
-    p.direct = !track && max_len <= kDirect && (int64_t)c->batch * c->heads * p.tiles <= (1 << 20);
+    const int64_t rows = (int64_t)c->batch * c->heads * p.tiles;
+    p.direct = !track && rows <= (1 << 20) && (max_len <= kDirect || (rows >= device_cus() && max_len <= 4 * rows));
     p.score_ld = (int)((max_len + 63) / 64 * 64);   // whole steps of a wave are written
     if (p.direct) return p;
-    const int64_t rows = (int64_t)c->batch * c->heads * p.tiles;
     // (the least step, whatever the type of the queries: the workspace does not depend on it)
     const int64_t steps = rows * ((max_len + kLeastStep - 1) / kLeastStep);
     p.groups = (int)std::max<int64_t>(1, std::min<int64_t>({steps, (int64_t)device_cus() * kGroupsPerCu, kMaxGroups}));
@@ -710,11 +718,11 @@ int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_
     a.scores = reinterpret_cast<float *>(ws + p.part + p.stat + p.first);
     a.q_ld = q_ld, a.out_ld = out_ld, a.mask_ld = mask_ld;
     a.hq = q_heads, a.G = q_heads / c->heads, a.tiles = p.tiles, a.tile_heads = p.tile_heads;
-    a.max_len = (int)max_len, a.score_ld = p.score_ld, a.step_log = ilog2(step_of(c->head_dim > 128 ? 256 : c->head_dim > 64 ? 128 : 64, c->dtype == RQ_I8, bf16));
+    a.max_len = (int)max_len, a.score_ld = p.score_ld, a.step_log = ilog2(step_of(c->head_dim > 128 ? 256 : c->head_dim > 64 ? 128 : 64, c->dtype == RQ_I8, bf16, p.direct));
     a.scale2 = scale * 1.4426950408889634f;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const unsigned groups = p.direct ? (unsigned)c->batch * c->heads * p.tiles : (unsigned)p.groups;
-    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(groups), dim3(kThreads), 0, s, a); };
+    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(groups), dim3(waves_of(p.direct) * 64), 0, s, a); };
     auto pick = [&](auto dp, auto exact, auto i8, auto io) {
         constexpr int DP = decltype(dp)::value;
         constexpr bool E = decltype(exact)::value, I = decltype(i8)::value, B = decltype(io)::value;
