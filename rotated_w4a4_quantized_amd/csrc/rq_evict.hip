@@ -2,7 +2,12 @@
 //
 // Per (sequence, head) row of n slots: the keep first in the order (protected,
 // weight descending, slot ascending) stay.  Survivors above `keep` move into
-// the free slots below it, so a move never reads what another one writes.
+// the free slots below it: a move never reads what another one writes, and a
+// cache a little over its budget moves a few tokens instead of closing ranks.
+//
+// Selection is one workgroup a row and bound by its chain of barriers and by
+// reading weights and positions once; the moves are a copy, bound by HBM where
+// they are many.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -15,6 +20,9 @@ namespace {
 
 using attn::Cache;
 
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+
 struct Args {
     Cache c;
     const int32_t *lens;
@@ -23,7 +31,7 @@ struct Args {
     int32_t *count;      // [rows] moves of a row
     int32_t *moves;      // [rows][2][most] free slots, then survivors
     int64_t slots;
-    int32_t max_len, keep, recent, sink, most;
+    int32_t max_len, keep, recent, sink, most, row_bytes;
 };
 
 // Order-preserving map of a weight to unsigned: NaN lowest, protected highest.
@@ -35,133 +43,266 @@ __device__ __forceinline__ uint32_t key_of(float w, bool held) {
     return b == 0x80000000u ? 0x80000000u : b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 1024, kSelWaves = kThreads / 64;
 
-__device__ int block_sum(int v, int *part) {
-    for (int o = 1; o < 64; o *= 2) v += __shfl_xor(v, o);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-    __syncthreads();
-    int s = 0;
-    for (int i = 0; i < kThreads / 64; ++i) s += part[i];
-    __syncthreads();
-    return s;
-}
-// exclusive prefix over the threads
-__device__ int block_scan(int v, int *part, int &total) {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    int x = v;
-    for (int o = 1; o < 64; o *= 2) {
-        const int y = __shfl_up(x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 63) part[w] = x;
-    __syncthreads();
-    int before = 0;
-    total = 0;
-    for (int i = 0; i < kThreads / 64; ++i) {
-        if (i < w) before += part[i];
-        total += part[i];
-    }
-    __syncthreads();
-    return before + x - v;
-}
-
-__global__ void __launch_bounds__(kThreads) select_kernel(Args a) {
-    __shared__ int part[kThreads / 64];
-    const int row = blockIdx.x, b = row / a.c.heads, t = threadIdx.x;
-    const int n = min(max(a.lens[b], 0), a.max_len);
-    const float *w = a.c.weight + row * a.slots;
-    const int32_t *pos = a.c.pos + row * a.slots;
-    float *wo = a.weight_out + row * a.slots;
-    int32_t *po = a.pos_out + row * a.slots;
-    if (n <= a.keep) {
-        for (int j = t; j < n; j += kThreads) {
-            wo[j] = w[j];
-            po[j] = pos[j];
+// Copies the moves [first, last) of a row by the whole workgroup (THREADS), VEC
+// bytes a load: the rows of 64 moves at a time through s_rows, then their keys
+// and values as one run of vectors, four of a thread in flight.
+template <int VEC, int THREADS>
+__device__ void copy_moves(const Args &a, int b, int h, const int32_t *free_list, const int32_t *up_list, int first, int last, int64_t (*s_rows)[64]) {
+    const int t = threadIdx.x;
+    for (int at = first; at < last; at += 64) {
+        const int n = min(64, last - at);
+        if (t < n) {
+            const int64_t to = a.c.row(b, h, free_list[at + t]), from = a.c.row(b, h, up_list[at + t]);
+            const bool both = to >= 0 && from >= 0;
+            s_rows[0][t] = both ? to : -1;
+            s_rows[1][t] = from;
+            if (both && a.c.k_scale) {
+                a.c.k_scale[to] = a.c.k_scale[from];
+                a.c.v_scale[to] = a.c.v_scale[from];
+            }
         }
+        __syncthreads();
+        const int vecs = a.row_bytes / VEC, all = n * vecs * 2;
+        constexpr int U = 4;
+        for (int i0 = t; i0 < all; i0 += THREADS * U) {
+            u4 x[U];
+            char *to[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * THREADS;
+                to[u] = nullptr;
+                if (i >= all) continue;
+                const int m = i / (2 * vecs), v = i - m * 2 * vecs;
+                if (s_rows[0][m] < 0) continue;
+                char *base = static_cast<char *>(v < vecs ? a.c.k : a.c.v);
+                const int off = (v < vecs ? v : v - vecs) * VEC;
+                to[u] = base + s_rows[0][m] * a.row_bytes + off;
+                const char *from = base + s_rows[1][m] * a.row_bytes + off;
+                if constexpr (VEC == 16) x[u] = *reinterpret_cast<const u4 *>(from);
+                else {
+                    const u2 y = *reinterpret_cast<const u2 *>(from);
+                    x[u][0] = y[0];
+                    x[u][1] = y[1];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (to[u]) {
+                    if constexpr (VEC == 16) *reinterpret_cast<u4 *>(to[u]) = x[u];
+                    else *reinterpret_cast<u2 *>(to[u]) = u2{x[u][0], x[u][1]};
+                }
+        }
+        __syncthreads();
+    }
+}
+
+// One row.  Wave w owns the slots (w iters + i) 64 + lane, i < iters, so slots
+// ascend along waves, steps and lanes: ranks within a wave are counts of ballot
+// bits, and one exchange between the waves turns them into ranks in the row.
+// K > 0: up to K steps, weights and positions held in registers and read once;
+// K == 0: any length, read again in each pass (they come from the caches).
+//
+// The keep-th largest key is found by digits of 11, 11 and 10 bits, each with a
+// histogram of the keys that share the digits before; it ends early when a
+// digit's keys are all needed.
+template <int K, bool FUSED>
+__global__ void __launch_bounds__(kThreads) select_kernel(Args a) {
+    __shared__ uint32_t s_hist[3][2048];
+    __shared__ int s_wave[4][kSelWaves];
+    __shared__ uint32_t s_digit;
+    __shared__ int s_above, s_in;
+    __shared__ int64_t s_rows[2][64];
+    const int row = blockIdx.x, b = row / a.c.heads, t = threadIdx.x, lane = t & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int n = min(max(a.lens[b], 0), a.max_len);
+    const float *w_in = a.c.weight + row * a.slots;
+    const int32_t *p_in = a.c.pos + row * a.slots;
+    float *w_out = a.weight_out + row * a.slots;
+    int32_t *p_out = a.pos_out + row * a.slots;
+    if (FUSED && row == b * a.c.heads && t == 0) a.lens_out[b] = min(n, a.keep);
+    if (n <= a.keep) {
+        if (w_out != w_in || p_out != p_in)
+            for (int j = t; j < n; j += kThreads) {
+                w_out[j] = w_in[j];
+                p_out[j] = p_in[j];
+            }
         if (t == 0) a.count[row] = 0;
         return;
     }
+    const int iters = (n + kThreads - 1) / kThreads;
+    const int base = wave * iters * 64 + lane;
+    constexpr int R = K ? K : 1;
+    float wr[R];
+    int32_t pr[R];           // (until the newest is known)
     int newest = -1;
-    for (int j = t; j < n; j += kThreads) newest = max(newest, pos[j]);
+    if constexpr (K > 0) {
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const int j = base + i * 64;
+            const bool in = i < iters && j < n;
+            wr[i] = in ? w_in[j] : 0.0f;
+            pr[i] = in ? p_in[j] : -1;
+            newest = max(newest, pr[i]);
+        }
+    } else
+        for (int i = 0; i < iters; ++i)
+            if (base + i * 64 < n) newest = max(newest, p_in[base + i * 64]);
+    for (int i = t; i < 3 * 2048; i += kThreads) (&s_hist[0][0])[i] = 0;
     for (int o = 1; o < 64; o *= 2) newest = max(newest, __shfl_xor(newest, o));
-    if ((t & 63) == 0) part[t >> 6] = newest;
+    if (lane == 0) s_wave[0][wave] = newest;
     __syncthreads();
-    for (int i = 0; i < kThreads / 64; ++i) newest = max(newest, part[i]);
-    __syncthreads();
+    for (int i = 0; i < kSelWaves; ++i) newest = max(newest, s_wave[0][i]);
     const int from = newest - a.recent;
-    auto key = [&](int j) { return key_of(w[j], pos[j] < a.sink || pos[j] > from); };
-    // the largest key that at least `keep` keys reach
+    auto protects = [&](int32_t p) { return p < a.sink || p > from; };
+    uint32_t held = 0;       // bit i: slot i of this thread is protected
+    if constexpr (K > 0) {
+#pragma unroll
+        for (int i = 0; i < K; ++i) held |= (uint32_t)protects(pr[i]) << i;
+    }
+    // f(j, the slot exists, its key) for this thread's slots; all lanes of a wave
+    // take part in every step
+    auto each = [&](auto f) {
+        if constexpr (K > 0) {
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+                if (i < iters) f(base + i * 64, base + i * 64 < n, key_of(wr[i], held >> i & 1));
+        } else
+            for (int i = 0; i < iters; ++i) {
+                const int j = base + i * 64;
+                const bool in = j < n;
+                f(j, in, key_of(in ? w_in[j] : 0.0f, in && protects(p_in[j])));
+            }
+    };
+
+    // the threshold: keys above it stay, and the first `ties` keys equal to it
     uint32_t thr = 0;
-    for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t c = thr | (1u << bit);
-        int mine = 0;
-        for (int j = t; j < n; j += kThreads) mine += key(j) >= c;
-        if (block_sum(mine, part) >= a.keep) thr = c;
+    int need = a.keep;       // of the keys that share the digits found so far
+    bool all_in = false;
+    for (int pass = 0; pass < 3 && !all_in; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const uint32_t digits = pass == 2 ? 1024 : 2048;
+        const uint32_t seen = pass == 0 ? 0u : pass == 1 ? 0xffe00000u : 0xfffffc00u;
+        each([&](int, bool in, uint32_t k) {
+            if (in && (k & seen) == thr) atomicAdd(&s_hist[pass][(k >> shift) & (digits - 1)], 1u);
+        });
+        __syncthreads();
+        // thread t: digits 2047 - 2 t and below, from the top
+        const int d = 2046 - 2 * t;
+        const int hi = s_hist[pass][d + 1], lo = s_hist[pass][d];
+        int upto = hi + lo;
+        for (int o = 1; o < 64; o *= 2) {
+            const int y = __shfl_up(upto, o);
+            if (lane >= o) upto += y;
+        }
+        if (lane == 63) s_wave[1][wave] = upto;
+        __syncthreads();
+        for (int i = 0; i < wave; ++i) upto += s_wave[1][i];
+        const int above = upto - hi - lo;
+        if (above < need && need <= upto) {   // one thread
+            const bool in_hi = need <= above + hi;
+            s_digit = in_hi ? d + 1 : d;
+            s_above = in_hi ? above : above + hi;
+            s_in = in_hi ? hi : lo;
+        }
+        __syncthreads();
+        thr |= s_digit << shift;
+        need -= s_above;
+        all_in = need == s_in;
     }
-    int above = 0;
-    for (int j = t; j < n; j += kThreads) above += key(j) > thr;
-    int ties = a.keep - block_sum(above, part);   // of the keys at the threshold, the lowest slots
-    // (weights and positions of the places below keep are written by the move: they may be the inputs)
-    int free_at = 0, up_at = 0;
+    // (ended early: every key with these digits stays, and thr is their lower bound)
+    const int ties = all_in ? 0x7fffffff : need;
+    // Ended early, keys from thr up stay; otherwise those above it and some ties.
+    int tied = 0;
+    if (!all_in) each([&](int, bool in, uint32_t k) { tied += __popcll(__ballot(in && k == thr)); });
+    if (lane == 0) s_wave[2][wave] = tied;
+    __syncthreads();
+    int tie_at = 0;
+    for (int i = 0; i < wave; ++i) tie_at += s_wave[2][i];
+    const uint64_t below = (1ull << lane) - 1;
+    auto walk = [&](auto f) {   // f(j, stays, is a free place, is a survivor from above)
+        int at = tie_at;
+        each([&](int j, bool in, uint32_t k) {
+            bool stays;
+            if (all_in) stays = in && k >= thr;
+            else {
+                const bool tie = in && k == thr;
+                const uint64_t m = __ballot(tie);
+                stays = in && (k > thr || (tie && at + __popcll(m & below) < ties));
+                at += __popcll(m);
+            }
+            f(j, stays, in && !stays && j < a.keep, stays && j >= a.keep);
+        });
+    };
+    int frees = 0, ups = 0;
+    walk([&](int, bool, bool is_free, bool is_up) {
+        frees += __popcll(__ballot(is_free));
+        ups += __popcll(__ballot(is_up));
+    });
+    if (lane == 0) {
+        s_wave[0][wave] = frees;
+        s_wave[3][wave] = ups;
+    }
+    __syncthreads();
+    int free_at = 0, up_at = 0, total = 0;
+    for (int i = 0; i < kSelWaves; ++i) {
+        if (i < wave) free_at += s_wave[0][i], up_at += s_wave[3][i];
+        total += s_wave[3][i];
+    }
     int32_t *free_list = a.moves + (int64_t)row * 2 * a.most, *up_list = free_list + a.most;
-    for (int base = 0; base < n; base += kThreads) {
-        const int j = base + t;
-        const uint32_t k = j < n ? key(j) : 0;
-        int total;
-        const int tied = j < n && k == thr;
-        const int rank = block_scan(tied, part, total);
-        const bool kept = j < n && (k > thr || (tied && rank < ties));
-        ties -= min(total, ties);
-        const int is_free = j < a.keep && !kept, is_up = j >= a.keep && j < n && kept;
-        const int f = block_scan(is_free, part, total) + free_at;
-        free_at += total;
-        const int u = block_scan(is_up, part, total) + up_at;
-        up_at += total;
-        if (is_free) free_list[f] = j;
-        if (is_up) up_list[u] = j;
+    walk([&](int j, bool, bool is_free, bool is_up) {
+        const uint64_t mf = __ballot(is_free), mu = __ballot(is_up);
+        if (is_free) free_list[free_at + __popcll(mf & below)] = j;
+        if (is_up) up_list[up_at + __popcll(mu & below)] = j;
+        free_at += __popcll(mf);
+        up_at += __popcll(mu);
+    });
+    if (t == 0) a.count[row] = total;
+    __threadfence_block();
+    __syncthreads();
+    // Weights and positions last: the places written may be the ones read above.
+    // (Written are the free places and, where the outputs are apart, what stays
+    // below keep; read is what stays, which in place nobody writes.)
+    if (w_out != w_in || p_out != p_in) {
+        walk([&](int j, bool stays, bool, bool is_up) {
+            if (stays && !is_up) {
+                w_out[j] = w_in[j];
+                p_out[j] = p_in[j];
+            }
+        });
+        __syncthreads();   // (one of the two may be in place, and without registers the walk reads both)
     }
-    if (t == 0) a.count[row] = up_at;
-    __threadfence_block();
-    __syncthreads();
-    if (wo != w || po != pos)
-        for (int j = t; j < a.keep; j += kThreads) {
-            wo[j] = w[j];
-            po[j] = pos[j];
-        }
-    __threadfence_block();
-    __syncthreads();
-    for (int i = t; i < up_at; i += kThreads) {
-        wo[free_list[i]] = w[up_list[i]];
-        po[free_list[i]] = pos[up_list[i]];
+    for (int i = t; i < total; i += kThreads) {
+        const int to = free_list[i], up = up_list[i];
+        w_out[to] = w_in[up];
+        p_out[to] = p_in[up];
+    }
+    if constexpr (FUSED) {
+        const int h = row - b * a.c.heads;
+        if (a.row_bytes % 16 == 0) copy_moves<16, kThreads>(a, b, h, free_list, up_list, 0, total, s_rows);
+        else copy_moves<8, kThreads>(a, b, h, free_list, up_list, 0, total, s_rows);
     }
 }
 
-// Keys and values of one row's moves: a wave per move.
-__global__ void __launch_bounds__(256) move_kernel(Args a, int bytes) {
-    const int row = blockIdx.y, b = row / a.c.heads, h = row % a.c.heads, lane = threadIdx.x & 63;
+constexpr int kChunk = 64;   // moves of a workgroup
+
+// Keys and values of the moves, and the lengths: nothing reads those any more, so
+// lens_out may be lens.
+template <int VEC>
+__global__ void __launch_bounds__(256) move_kernel(Args a, int chunks, int lens_groups) {
+    __shared__ int64_t s_rows[2][64];
+    if ((int)blockIdx.x < lens_groups) {
+        const int b = blockIdx.x * 256 + threadIdx.x;
+        if (b < a.c.batch) a.lens_out[b] = min(min(max(a.lens[b], 0), a.max_len), a.keep);
+        return;
+    }
+    const int id = blockIdx.x - lens_groups, row = id / chunks, first = (id - row * chunks) * kChunk;
     const int count = a.count[row];
+    if (first >= count) return;
+    const int b = row / a.c.heads, h = row - b * a.c.heads;
     const int32_t *free_list = a.moves + (int64_t)row * 2 * a.most, *up_list = free_list + a.most;
-    for (int i = blockIdx.x * 4 + (threadIdx.x >> 6); i < count; i += gridDim.x * 4) {
-        const int64_t to = a.c.row(b, h, free_list[i]), from = a.c.row(b, h, up_list[i]);
-        if (to < 0 || from < 0) continue;
-        for (int d = lane * 8; d < a.c.D * bytes; d += 512) {
-            *reinterpret_cast<uint2 *>(static_cast<char *>(a.c.k) + to * a.c.D * bytes + d) =
-                *reinterpret_cast<const uint2 *>(static_cast<const char *>(a.c.k) + from * a.c.D * bytes + d);
-            *reinterpret_cast<uint2 *>(static_cast<char *>(a.c.v) + to * a.c.D * bytes + d) =
-                *reinterpret_cast<const uint2 *>(static_cast<const char *>(a.c.v) + from * a.c.D * bytes + d);
-        }
-        if (bytes == 1 && lane == 0) {
-            a.c.k_scale[to] = a.c.k_scale[from];
-            a.c.v_scale[to] = a.c.v_scale[from];
-        }
-    }
-}
-
-// Last: nothing reads lens after it, so lens_out may be lens.
-__global__ void __launch_bounds__(256) lens_kernel(Args a) {
-    const int b = blockIdx.x * 256 + threadIdx.x;
-    if (b < a.c.batch) a.lens_out[b] = min(min(max(a.lens[b], 0), a.max_len), a.keep);
+    copy_moves<VEC, 256>(a, b, h, free_list, up_list, first, min(count, first + kChunk), s_rows);
 }
 
 int most_moves(int keep, int64_t max_len) {
@@ -187,12 +328,30 @@ int launch_cache_evict(const rq_kv_cache *c, const int32_t *lens, int64_t max_le
     a.slots = (int64_t)c->table_ld * c->page;
     a.max_len = (int)max_len, a.keep = keep, a.recent = recent, a.sink = sink;
     a.most = most_moves(keep, max_len);
+    a.row_bytes = c->head_dim * (c->dtype == RQ_I8 ? 1 : 2);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    hipLaunchKernelGGL(select_kernel, dim3(rows), dim3(kThreads), 0, s, a);
-    if (a.most > 0)
-        hipLaunchKernelGGL(move_kernel, dim3((unsigned)std::min((a.most + 3) / 4, 256), rows), dim3(256), 0, s, a,
-                           c->dtype == RQ_I8 ? 1 : 2);
-    hipLaunchKernelGGL(lens_kernel, dim3((c->batch + 255) / 256), dim3(256), 0, s, a);
+    // Few moves are done by the workgroup that found them.  (Not with lens_out in
+    // place: another row of the sequence may still have to read its length.)
+    const bool fused = a.most <= 256 && lens_out != lens;
+    const int64_t chunks = (a.most + kChunk - 1) / kChunk, lens_groups = (c->batch + 255) / 256;
+    // (a launch holds 2^32 threads)
+    if (rows > (1 << 22) - 1 || chunks * rows + lens_groups > (1 << 24) - 1) return (int)hipErrorInvalidValue;
+    auto select = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(rows), dim3(kThreads), 0, s, a); };
+    auto pick = [&](auto f) {
+        constexpr bool F = decltype(f)::value;
+        const int64_t iters = (max_len + kThreads - 1) / kThreads;
+        if (iters <= 2) select(select_kernel<2, F>);
+        else if (iters <= 8) select(select_kernel<8, F>);
+        else if (iters <= 32) select(select_kernel<32, F>);
+        else select(select_kernel<0, F>);
+    };
+    if (fused) pick(std::true_type{});
+    else {
+        pick(std::false_type{});
+        const dim3 grid((unsigned)(chunks * rows + lens_groups));
+        if (a.row_bytes % 16 == 0) hipLaunchKernelGGL(move_kernel<16>, grid, dim3(256), 0, s, a, (int)chunks, (int)lens_groups);
+        else hipLaunchKernelGGL(move_kernel<8>, grid, dim3(256), 0, s, a, (int)chunks, (int)lens_groups);
+    }
     return (int)hipGetLastError();
 }
 
