@@ -22,6 +22,7 @@ using attn::Cache;
 
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef int32_t i4 __attribute__((ext_vector_type(4)));
 
 struct Args {
     Cache c;
@@ -43,16 +44,53 @@ __device__ __forceinline__ uint32_t key_of(float w, bool held) {
     return b == 0x80000000u ? 0x80000000u : b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// moves of a row, at most, that the workgroup which found them copies too
+constexpr int kFused = 256;
 constexpr int kThreads = 1024, kSelWaves = kThreads / 64;
 
+// inclusive sum over the lanes up to this one: shifts within rows of 16, then
+// the rows' last lanes passed on
+__device__ __forceinline__ int wave_scan(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
+    return x;
+}
+// the largest of the lanes, in lane 63
+__device__ __forceinline__ int wave_max63(int x) {
+    x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x111, 0xf, 0xf, false));
+    x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x112, 0xf, 0xf, false));
+    x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x114, 0xf, 0xf, false));
+    x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x118, 0xf, 0xf, false));
+    x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x142, 0xa, 0xf, false));
+    x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x143, 0xc, 0xf, false));
+    return x;
+}
+// sums of v[i] over the waves before this one and over all
+__device__ __forceinline__ void over_waves(const int *v, int wave, int &before, int &all) {
+    before = all = 0;
+#pragma unroll
+    for (int i = 0; i < kSelWaves; ++i) {
+        const int x = v[i];
+        before += i < wave ? x : 0;
+        all += x;
+    }
+}
+// Place of a digit's count: 32 digits and a gap of 4 words, so that lanes that
+// each read 32 digits in a row meet different banks.
+__device__ __forceinline__ int place_of(uint32_t d) { return (int)(d + (d >> 5) * 4); }
+
 // Copies the moves [first, last) of a row by the whole workgroup (THREADS), VEC
-// bytes a load: the rows of 64 moves at a time through s_rows, then their keys
-// and values as one run of vectors, four of a thread in flight.
-template <int VEC, int THREADS>
-__device__ void copy_moves(const Args &a, int b, int h, const int32_t *free_list, const int32_t *up_list, int first, int last, int64_t (*s_rows)[64]) {
+// bytes a load: the rows of ROWS moves at a time through s_rows, then their keys
+// and values as one run of vectors, U of a thread in flight.
+template <int VEC, int THREADS, int ROWS, int U>
+__device__ void copy_moves(const Args &a, int b, int h, const int32_t *free_list, const int32_t *up_list, int first, int last, int64_t (*s_rows)[ROWS]) {
     const int t = threadIdx.x;
-    for (int at = first; at < last; at += 64) {
-        const int n = min(64, last - at);
+    for (int at = first; at < last; at += ROWS) {
+        const int n = min(ROWS, last - at);
         if (t < n) {
             const int64_t to = a.c.row(b, h, free_list[at + t]), from = a.c.row(b, h, up_list[at + t]);
             const bool both = to >= 0 && from >= 0;
@@ -65,7 +103,6 @@ __device__ void copy_moves(const Args &a, int b, int h, const int32_t *free_list
         }
         __syncthreads();
         const int vecs = a.row_bytes / VEC, all = n * vecs * 2;
-        constexpr int U = 4;
         for (int i0 = t; i0 < all; i0 += THREADS * U) {
             u4 x[U];
             char *to[U];
@@ -109,11 +146,11 @@ __device__ void copy_moves(const Args &a, int b, int h, const int32_t *free_list
 // digit's keys are all needed.
 template <int K, bool FUSED>
 __global__ void __launch_bounds__(kThreads) select_kernel(Args a) {
-    __shared__ uint32_t s_hist[3][2048];
-    __shared__ int s_wave[4][kSelWaves];
+    __shared__ __align__(16) int s_hist[3][2048 + 64 * 4];
+    __shared__ __align__(16) int s_wave[4][kSelWaves];
     __shared__ uint32_t s_digit;
     __shared__ int s_above, s_in;
-    __shared__ int64_t s_rows[2][64];
+    __shared__ int64_t s_rows[2][FUSED ? kFused : 1];
     const int row = blockIdx.x, b = row / a.c.heads, t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int n = min(max(a.lens[b], 0), a.max_len);
@@ -134,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(Args a) {
     const int iters = (n + kThreads - 1) / kThreads;
     const int base = wave * iters * 64 + lane;
     constexpr int R = K ? K : 1;
-    float wr[R];
+    uint32_t kr[R];
     int32_t pr[R];           // (until the newest is known)
     int newest = -1;
     if constexpr (K > 0) {
@@ -142,24 +179,25 @@ __global__ void __launch_bounds__(kThreads) select_kernel(Args a) {
         for (int i = 0; i < K; ++i) {
             const int j = base + i * 64;
             const bool in = i < iters && j < n;
-            wr[i] = in ? w_in[j] : 0.0f;
+            kr[i] = in ? __builtin_bit_cast(uint32_t, w_in[j]) : 0u;
             pr[i] = in ? p_in[j] : -1;
             newest = max(newest, pr[i]);
         }
     } else
         for (int i = 0; i < iters; ++i)
             if (base + i * 64 < n) newest = max(newest, p_in[base + i * 64]);
-    for (int i = t; i < 3 * 2048; i += kThreads) (&s_hist[0][0])[i] = 0;
-    for (int o = 1; o < 64; o *= 2) newest = max(newest, __shfl_xor(newest, o));
-    if (lane == 0) s_wave[0][wave] = newest;
+    for (int i = t; i < 3 * (2048 + 64 * 4); i += kThreads) (&s_hist[0][0])[i] = 0;
+    newest = wave_max63(newest);
+    if (lane == 63) s_wave[0][wave] = newest;
     __syncthreads();
+#pragma unroll
     for (int i = 0; i < kSelWaves; ++i) newest = max(newest, s_wave[0][i]);
+    newest = __builtin_amdgcn_readlane(newest, 63);
     const int from = newest - a.recent;
     auto protects = [&](int32_t p) { return p < a.sink || p > from; };
-    uint32_t held = 0;       // bit i: slot i of this thread is protected
     if constexpr (K > 0) {
 #pragma unroll
-        for (int i = 0; i < K; ++i) held |= (uint32_t)protects(pr[i]) << i;
+        for (int i = 0; i < K; ++i) kr[i] = key_of(__builtin_bit_cast(float, kr[i]), protects(pr[i]));
     }
     // f(j, the slot exists, its key) for this thread's slots; all lanes of a wave
     // take part in every step
@@ -167,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(Args a) {
         if constexpr (K > 0) {
 #pragma unroll
             for (int i = 0; i < K; ++i)
-                if (i < iters) f(base + i * 64, base + i * 64 < n, key_of(wr[i], held >> i & 1));
+                if (i < iters) f(base + i * 64, base + i * 64 < n, kr[i]);
         } else
             for (int i = 0; i < iters; ++i) {
                 const int j = base + i * 64;
@@ -185,26 +223,37 @@ __global__ void __launch_bounds__(kThreads) select_kernel(Args a) {
         const uint32_t digits = pass == 2 ? 1024 : 2048;
         const uint32_t seen = pass == 0 ? 0u : pass == 1 ? 0xffe00000u : 0xfffffc00u;
         each([&](int, bool in, uint32_t k) {
-            if (in && (k & seen) == thr) atomicAdd(&s_hist[pass][(k >> shift) & (digits - 1)], 1u);
+            if (in && (k & seen) == thr) atomicAdd(&s_hist[pass][place_of((k >> shift) & (digits - 1))], 1);
         });
         __syncthreads();
-        // thread t: digits 2047 - 2 t and below, from the top
-        const int d = 2046 - 2 * t;
-        const int hi = s_hist[pass][d + 1], lo = s_hist[pass][d];
-        int upto = hi + lo;
-        for (int o = 1; o < 64; o *= 2) {
-            const int y = __shfl_up(upto, o);
-            if (lane >= o) upto += y;
-        }
-        if (lane == 63) s_wave[1][wave] = upto;
-        __syncthreads();
-        for (int i = 0; i < wave; ++i) upto += s_wave[1][i];
-        const int above = upto - hi - lo;
-        if (above < need && need <= upto) {   // one thread
-            const bool in_hi = need <= above + hi;
-            s_digit = in_hi ? d + 1 : d;
-            s_above = in_hi ? above : above + hi;
-            s_in = in_hi ? hi : lo;
+        // the first wave finds the digit: lane l has digits 2047 - 32 l downwards
+        if (wave == 0) {
+            const int top = 2047 - 32 * lane;
+            int c[32], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const i4 v = *reinterpret_cast<const i4 *>(&s_hist[pass][place_of(top - 31) + 4 * i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    c[31 - 4 * i - e] = v[e];   // c[x]: digit top - x
+                    sum += v[e];
+                }
+            }
+            const int upto = wave_scan(sum);
+            int above = upto - sum;
+            if (above < need && need <= upto) {   // one lane
+                int x = 0, in = c[0];
+#pragma unroll
+                for (int y = 1; y < 32; ++y)
+                    if (above + in < need) {
+                        above += in;
+                        in = c[y];
+                        x = y;
+                    }
+                s_digit = top - x;
+                s_above = above;
+                s_in = in;
+            }
         }
         __syncthreads();
         thr |= s_digit << shift;
@@ -214,15 +263,18 @@ __global__ void __launch_bounds__(kThreads) select_kernel(Args a) {
     // (ended early: every key with these digits stays, and thr is their lower bound)
     const int ties = all_in ? 0x7fffffff : need;
     // Ended early, keys from thr up stay; otherwise those above it and some ties.
-    int tied = 0;
-    if (!all_in) each([&](int, bool in, uint32_t k) { tied += __popcll(__ballot(in && k == thr)); });
-    if (lane == 0) s_wave[2][wave] = tied;
-    __syncthreads();
     int tie_at = 0;
-    for (int i = 0; i < wave; ++i) tie_at += s_wave[2][i];
+    if (!all_in) {
+        int tied = 0, all;
+        each([&](int, bool in, uint32_t k) { tied += __popcll(__ballot(in && k == thr)); });
+        if (lane == 0) s_wave[2][wave] = tied;
+        __syncthreads();
+        over_waves(s_wave[2], wave, tie_at, all);
+    }
     const uint64_t below = (1ull << lane) - 1;
-    auto walk = [&](auto f) {   // f(j, stays, is a free place, is a survivor from above)
-        int at = tie_at;
+    uint32_t stay_bits = 0;   // K > 0: of this thread's slots, so that they are found once
+    auto walk = [&](auto f) {   // f(i, the slot stays, is a free place, is a survivor from above)
+        int at = tie_at, i = 0;
         each([&](int j, bool in, uint32_t k) {
             bool stays;
             if (all_in) stays = in && k >= thr;
@@ -232,46 +284,60 @@ __global__ void __launch_bounds__(kThreads) select_kernel(Args a) {
                 stays = in && (k > thr || (tie && at + __popcll(m & below) < ties));
                 at += __popcll(m);
             }
-            f(j, stays, in && !stays && j < a.keep, stays && j >= a.keep);
+            f(i++, j, stays, in && !stays && j < a.keep, stays && j >= a.keep);
         });
     };
     int frees = 0, ups = 0;
-    walk([&](int, bool, bool is_free, bool is_up) {
+    walk([&](int i, int, bool stays, bool is_free, bool is_up) {
+        if (K > 0) stay_bits |= (uint32_t)stays << i;
         frees += __popcll(__ballot(is_free));
         ups += __popcll(__ballot(is_up));
     });
     if (lane == 0) {
-        s_wave[0][wave] = frees;
+        s_wave[1][wave] = frees;
         s_wave[3][wave] = ups;
     }
     __syncthreads();
-    int free_at = 0, up_at = 0, total = 0;
-    for (int i = 0; i < kSelWaves; ++i) {
-        if (i < wave) free_at += s_wave[0][i], up_at += s_wave[3][i];
-        total += s_wave[3][i];
-    }
+    int free_at, up_at, total, all_free;
+    over_waves(s_wave[1], wave, free_at, all_free);
+    over_waves(s_wave[3], wave, up_at, total);
     int32_t *free_list = a.moves + (int64_t)row * 2 * a.most, *up_list = free_list + a.most;
-    walk([&](int j, bool, bool is_free, bool is_up) {
+    auto list = [&](int j, bool is_free, bool is_up) {
         const uint64_t mf = __ballot(is_free), mu = __ballot(is_up);
         if (is_free) free_list[free_at + __popcll(mf & below)] = j;
         if (is_up) up_list[up_at + __popcll(mu & below)] = j;
         free_at += __popcll(mf);
         up_at += __popcll(mu);
-    });
+    };
+    if constexpr (K > 0) {
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            if (i < iters) {
+                const int j = base + i * 64;
+                const bool stays = stay_bits >> i & 1;
+                list(j, j < n && !stays && j < a.keep, stays && j >= a.keep);
+            }
+    } else
+        walk([&](int, int j, bool, bool is_free, bool is_up) { list(j, is_free, is_up); });
     if (t == 0) a.count[row] = total;
     __threadfence_block();
     __syncthreads();
-    // Weights and positions last: the places written may be the ones read above.
-    // (Written are the free places and, where the outputs are apart, what stays
-    // below keep; read is what stays, which in place nobody writes.)
+    // Weights and positions last, for the places written may be the ones read
+    // above: apart from the inputs, first what lies below keep; then the moves,
+    // which fill every place there that did not stay.
     if (w_out != w_in || p_out != p_in) {
-        walk([&](int j, bool stays, bool, bool is_up) {
-            if (stays && !is_up) {
-                w_out[j] = w_in[j];
-                p_out[j] = p_in[j];
-            }
-        });
-        __syncthreads();   // (one of the two may be in place, and without registers the walk reads both)
+        for (int j = t * 4; j < a.keep; j += kThreads * 4) {
+            if (j + 4 <= a.keep) {
+                *reinterpret_cast<u4 *>(w_out + j) = *reinterpret_cast<const u4 *>(w_in + j);
+                *reinterpret_cast<u4 *>(p_out + j) = *reinterpret_cast<const u4 *>(p_in + j);
+            } else
+                for (int e = j; e < a.keep; ++e) {
+                    w_out[e] = w_in[e];
+                    p_out[e] = p_in[e];
+                }
+        }
+        __threadfence_block();
+        __syncthreads();
     }
     for (int i = t; i < total; i += kThreads) {
         const int to = free_list[i], up = up_list[i];
@@ -280,18 +346,18 @@ __global__ void __launch_bounds__(kThreads) select_kernel(Args a) {
     }
     if constexpr (FUSED) {
         const int h = row - b * a.c.heads;
-        if (a.row_bytes % 16 == 0) copy_moves<16, kThreads>(a, b, h, free_list, up_list, 0, total, s_rows);
-        else copy_moves<8, kThreads>(a, b, h, free_list, up_list, 0, total, s_rows);
+        if (a.row_bytes % 16 == 0) copy_moves<16, kThreads, kFused, 4>(a, b, h, free_list, up_list, 0, total, s_rows);
+        else copy_moves<8, kThreads, kFused, 4>(a, b, h, free_list, up_list, 0, total, s_rows);
     }
 }
 
-constexpr int kChunk = 64;   // moves of a workgroup
+constexpr int kChunk = 64;   // moves of a workgroup (32 to 128 measured alike)
 
 // Keys and values of the moves, and the lengths: nothing reads those any more, so
 // lens_out may be lens.
 template <int VEC>
 __global__ void __launch_bounds__(256) move_kernel(Args a, int chunks, int lens_groups) {
-    __shared__ int64_t s_rows[2][64];
+    __shared__ int64_t s_rows[2][kChunk];
     if ((int)blockIdx.x < lens_groups) {
         const int b = blockIdx.x * 256 + threadIdx.x;
         if (b < a.c.batch) a.lens_out[b] = min(min(max(a.lens[b], 0), a.max_len), a.keep);
@@ -302,7 +368,7 @@ __global__ void __launch_bounds__(256) move_kernel(Args a, int chunks, int lens_
     if (first >= count) return;
     const int b = row / a.c.heads, h = row - b * a.c.heads;
     const int32_t *free_list = a.moves + (int64_t)row * 2 * a.most, *up_list = free_list + a.most;
-    copy_moves<VEC, 256>(a, b, h, free_list, up_list, first, min(count, first + kChunk), s_rows);
+    copy_moves<VEC, 256, kChunk, 4>(a, b, h, free_list, up_list, first, min(count, first + kChunk), s_rows);
 }
 
 int most_moves(int keep, int64_t max_len) {
@@ -332,7 +398,7 @@ int launch_cache_evict(const rq_kv_cache *c, const int32_t *lens, int64_t max_le
     hipStream_t s = static_cast<hipStream_t>(stream);
     // Few moves are done by the workgroup that found them.  (Not with lens_out in
     // place: another row of the sequence may still have to read its length.)
-    const bool fused = a.most <= 256 && lens_out != lens;
+    const bool fused = a.most <= kFused && lens_out != lens;
     const int64_t chunks = (a.most + kChunk - 1) / kChunk, lens_groups = (c->batch + 255) / 256;
     // (a launch holds 2^32 threads)
     if (rows > (1 << 22) - 1 || chunks * rows + lens_groups > (1 << 24) - 1) return (int)hipErrorInvalidValue;
