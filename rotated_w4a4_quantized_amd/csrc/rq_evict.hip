@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(Args a) {
                 w_out[j] = w_in[j];
                 p_out[j] = p_in[j];
             }
-        if (t == 0) a.count[row] = 0;
+        if (!FUSED && t == 0) a.count[row] = 0;
         return;
     }
     const int iters = (n + kThreads - 1) / kThreads;
@@ -301,7 +301,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(Args a) {
     int free_at, up_at, total, all_free;
     over_waves(s_wave[1], wave, free_at, all_free);
     over_waves(s_wave[3], wave, up_at, total);
-    int32_t *free_list = a.moves + (int64_t)row * 2 * a.most, *up_list = free_list + a.most;
+    // the lists: here if this workgroup alone reads them
+    __shared__ int32_t s_list[2][FUSED ? kFused : 1];
+    int32_t *free_list = FUSED ? s_list[0] : a.moves + (int64_t)row * 2 * a.most;
+    int32_t *up_list = FUSED ? s_list[1] : free_list + a.most;
     auto list = [&](int j, bool is_free, bool is_up) {
         const uint64_t mf = __ballot(is_free), mu = __ballot(is_up);
         if (is_free) free_list[free_at + __popcll(mf & below)] = j;
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(Args a) {
             }
     } else
         walk([&](int, int j, bool, bool is_free, bool is_up) { list(j, is_free, is_up); });
-    if (t == 0) a.count[row] = total;
+    if (!FUSED && t == 0) a.count[row] = total;
     __threadfence_block();
     __syncthreads();
     // Weights and positions last, for the places written may be the ones read
