@@ -46,6 +46,7 @@ __device__ __forceinline__ uint32_t key_of(float w, bool held) {
 
 // moves of a row, at most, that the workgroup which found them copies too
 constexpr int kFused = 256;
+constexpr int kBatch = 8;   // steps whose loads are in flight together, where keys are not held
 constexpr int kThreads = 1024, kSelWaves = kThreads / 64;
 
 // inclusive sum over the lanes up to this one: shifts within rows of 16, then
@@ -207,10 +208,19 @@ __global__ void __launch_bounds__(kThreads) select_kernel(Args a) {
             for (int i = 0; i < K; ++i)
                 if (i < iters) f(base + i * 64, base + i * 64 < n, kr[i]);
         } else
-            for (int i = 0; i < iters; ++i) {
-                const int j = base + i * 64;
-                const bool in = j < n;
-                f(j, in, key_of(in ? w_in[j] : 0.0f, in && protects(p_in[j])));
+            for (int i0 = 0; i0 < iters; i0 += kBatch) {
+                float w[kBatch];
+                int32_t p[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int j = base + (i0 + u) * 64;
+                    const bool in = i0 + u < iters && j < n;
+                    w[u] = in ? w_in[j] : 0.0f;
+                    p[u] = in ? p_in[j] : 0;
+                }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+                    if (i0 + u < iters) f(base + (i0 + u) * 64, base + (i0 + u) * 64 < n, key_of(w[u], protects(p[u])));
             }
     };
 
@@ -226,33 +236,26 @@ __global__ void __launch_bounds__(kThreads) select_kernel(Args a) {
             if (in && (k & seen) == thr) atomicAdd(&s_hist[pass][place_of((k >> shift) & (digits - 1))], 1);
         });
         __syncthreads();
-        // the first wave finds the digit: lane l has digits 2047 - 32 l downwards
+        // the first wave finds the digit: the 32 that it is among (lane l has
+        // digits 2047 - 32 l downwards), then which of them (a lane each)
         if (wave == 0) {
-            const int top = 2047 - 32 * lane;
-            int c[32], sum = 0;
+            int sum = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const i4 v = *reinterpret_cast<const i4 *>(&s_hist[pass][place_of(top - 31) + 4 * i]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    c[31 - 4 * i - e] = v[e];   // c[x]: digit top - x
-                    sum += v[e];
-                }
+                const i4 v = *reinterpret_cast<const i4 *>(&s_hist[pass][place_of(2016 - 32 * lane) + 4 * i]);
+                sum += v[0] + v[1] + v[2] + v[3];
             }
-            const int upto = wave_scan(sum);
-            int above = upto - sum;
-            if (above < need && need <= upto) {   // one lane
-                int x = 0, in = c[0];
-#pragma unroll
-                for (int y = 1; y < 32; ++y)
-                    if (above + in < need) {
-                        above += in;
-                        in = c[y];
-                        x = y;
-                    }
+            int upto = wave_scan(sum);
+            const int group = __ffsll((long long)__ballot(upto >= need)) - 1;   // (the last sum is all keys)
+            const int above = __builtin_amdgcn_readlane(upto - sum, group);
+            const int top = 2047 - 32 * group;
+            const int one = lane < 32 ? s_hist[pass][place_of(top - lane)] : 0;
+            upto = above + wave_scan(one);
+            const int x = __ffsll((long long)__ballot(upto >= need)) - 1;
+            if (lane == x) {
                 s_digit = top - x;
-                s_above = above;
-                s_in = in;
+                s_above = upto - one;
+                s_in = one;
             }
         }
         __syncthreads();
@@ -342,10 +345,25 @@ __global__ void __launch_bounds__(kThreads) select_kernel(Args a) {
         __threadfence_block();
         __syncthreads();
     }
-    for (int i = t; i < total; i += kThreads) {
-        const int to = free_list[i], up = up_list[i];
-        w_out[to] = w_in[up];
-        p_out[to] = p_in[up];
+    for (int i0 = t; i0 < total; i0 += kThreads * 4) {   // (four moves of a thread in flight)
+        int to[4];
+        float w[4];
+        int32_t p[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kThreads;
+            const bool in = i < total;
+            to[u] = in ? free_list[i] : -1;
+            const int up = in ? up_list[i] : 0;
+            w[u] = w_in[up];
+            p[u] = p_in[up];
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (to[u] >= 0) {
+                w_out[to[u]] = w[u];
+                p_out[to[u]] = p[u];
+            }
     }
     if constexpr (FUSED) {
         const int h = row - b * a.c.heads;
