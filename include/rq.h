@@ -1,6 +1,8 @@
 /*
  * rq.h -- C ABI of librq, the MI355X (gfx950) rotated low-bit quantized
- * linear layer of diffusion-transformer inference.
+ * linear layer of diffusion-transformer inference, and the attention between
+ * such layers (head norm with rotation, paged cache, single-token attention,
+ * eviction: the last part of this file).
  *
  * The layer (pages: "TR-DQ: Time-Rotation Diffusion Quantization",
  * section 3.1 and Eq.(8)-(9); "OrbitQuant" abstract; "DiRotQ" abstract):
@@ -694,7 +696,8 @@ rq_status rq_qk_norm_rope(const rq_qk_norm *d, const void *qkv, int32_t dtype, i
 /*
  * Bytes of device workspace rq_paged_attention takes for this cache,
  * q_heads, max_len and track.  It depends on these arguments and the
- * device only, never on lengths or data.
+ * device only, never on lengths or data, and is no larger for a smaller
+ * max_len.
  * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_DTYPE.
  */
 rq_status rq_paged_attention_workspace_bytes(const rq_kv_cache *cache, int32_t q_heads,
@@ -740,7 +743,8 @@ rq_status rq_paged_attention(const rq_kv_cache *cache, const void *q, int32_t dt
                              size_t workspace_bytes, void *stream);
 
 /*
- * Bytes of device workspace rq_cache_evict takes.
+ * Bytes of device workspace rq_cache_evict takes (no more for a smaller
+ * max_len).
  * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_DTYPE.
  */
 rq_status rq_cache_evict_workspace_bytes(const rq_kv_cache *cache, int32_t keep, int64_t max_len,

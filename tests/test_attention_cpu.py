@@ -155,6 +155,23 @@ def test_workspace_sizes():
     assert L.rq_cache_evict_workspace_bytes(ctypes.byref(c), 10, 100, ctypes.byref(n)) == 0 and n.value > 0
 
 
+@pytest.mark.parametrize("batch,heads,q_heads", [(1, 1, 1), (1, 8, 32), (40, 8, 8), (600, 4, 32), (3, 2, 80)])
+@pytest.mark.parametrize("track", [0, 1])
+def test_workspace_does_not_shrink_with_max_len(batch, heads, q_heads, track):
+    """A caller that sizes its workspace for the longest call may make shorter ones."""
+    L = rq.load()
+    c = cache(batch=batch, heads=heads, table_ld=4096, page=16)
+    last = last_evict = 0
+    for max_len in [0, 1, 15, 64, 65, 128, 500, 512, 513, 1000, 2399, 2400, 2401, 5000, 9600, 20000, 65536]:
+        n = ctypes.c_size_t(0)
+        assert L.rq_paged_attention_workspace_bytes(ctypes.byref(c), q_heads, max_len, track, ctypes.byref(n)) == 0
+        assert n.value >= last, max_len
+        last = n.value
+        assert L.rq_cache_evict_workspace_bytes(ctypes.byref(c), 1000, max_len, ctypes.byref(n)) == 0
+        assert n.value >= last_evict
+        last_evict = n.value
+
+
 def test_binding_refusals():
     k = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
     table = torch.zeros(1, 4, dtype=torch.int32)
