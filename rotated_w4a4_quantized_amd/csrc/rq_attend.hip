@@ -38,7 +38,7 @@ struct Args {
                      // what a wave's store writes lies together
     float *part;     // [workgroups + rows][heads of a tile][D], unnormalized outputs
     float *stat;     // [workgroups + rows][heads of a tile][2], their maxima and sums
-    int64_t *first;  // [batch + 1]: steps of a head before each sequence; then steps of a workgroup
+    int32_t *ends;   // [rows][2]: the first and the last workgroup of a row with tokens
     int64_t q_ld, out_ld, mask_ld;
     int32_t hq, G, tiles, tile_heads, max_len, score_ld, step_log;
     float scale2;    // scale * log2(e)
@@ -186,14 +186,6 @@ __global__ void __launch_bounds__(waves_of(DIRECT) * 64) __attribute__((amdgpu_w
         const int64_t per = max((int64_t)1, (all * rows_of_seq + gridDim.x - 1) / gridDim.x);
         u = blockIdx.x * per;
         u_end = min(all * rows_of_seq, u + per);
-        if (blockIdx.x == 0) {
-            int64_t at = upto - mine;
-            for (int i = lo; i < hi; ++i) {
-                a.first[i] = at;
-                at += steps_of(a, length_of(a, i));
-            }
-            if (threadIdx.x == 0) a.first[a.c.batch] = per;
-        }
         if (u >= u_end) return;
         if ((upto - mine) * rows_of_seq <= u && u < upto * rows_of_seq) {   // one thread
             int64_t at = upto - mine;
@@ -517,6 +509,11 @@ __global__ void __launch_bounds__(waves_of(DIRECT) * 64) __attribute__((amdgpu_w
         }
     }
     if constexpr (DIRECT) return;
+    if (threadIdx.x == 0) {
+        int32_t *e = a.ends + ((int64_t)b * rows_of_seq + r) * 2;
+        if (step0 == 0) e[0] = blockIdx.x;
+        if (step0 + here == row_steps) e[1] = blockIdx.x;
+    }
     u += here;
     if (u >= u_end) return;
     // the next row with tokens
@@ -529,16 +526,41 @@ __global__ void __launch_bounds__(waves_of(DIRECT) * 64) __attribute__((amdgpu_w
     }
 }
 
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float from_lane(float x, float none) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, x), CTRL, ROWS, 0xf, false));
+}
+// (shifts within rows of 16 lanes, then the rows' last lanes passed on: lane 63 has all)
+__device__ __forceinline__ float wave_max(float x) {
+    x = fmaxf(x, from_lane<0x111, 0xf>(x, -INFINITY));
+    x = fmaxf(x, from_lane<0x112, 0xf>(x, -INFINITY));
+    x = fmaxf(x, from_lane<0x114, 0xf>(x, -INFINITY));
+    x = fmaxf(x, from_lane<0x118, 0xf>(x, -INFINITY));
+    x = fmaxf(x, from_lane<0x142, 0xa>(x, -INFINITY));
+    x = fmaxf(x, from_lane<0x143, 0xc>(x, -INFINITY));
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+}
+__device__ __forceinline__ float wave_sum(float x) {
+    x += from_lane<0x111, 0xf>(x, 0.0f);
+    x += from_lane<0x112, 0xf>(x, 0.0f);
+    x += from_lane<0x114, 0xf>(x, 0.0f);
+    x += from_lane<0x118, 0xf>(x, 0.0f);
+    x += from_lane<0x142, 0xa>(x, 0.0f);
+    x += from_lane<0x143, 0xc>(x, 0.0f);
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+}
 // Statistics of a head over its n parts, by one wave: all lanes get the maximum
 // and the sum relative to it.
-__device__ __forceinline__ void join_stats(const float *st, int n, int stride, int lane, float &M, float &L) {
-    M = -INFINITY;
-    for (int i = lane; i < n; i += 64) M = fmaxf(M, st[(int64_t)i * stride]);
-    for (int o = 1; o < 64; o *= 2) M = fmaxf(M, __shfl_xor(M, o));
-    L = 0.0f;
-    for (int i = lane; i < n; i += 64)
-        if (st[(int64_t)i * stride] != -INFINITY) L += st[(int64_t)i * stride + 1] * __builtin_amdgcn_exp2f(st[(int64_t)i * stride] - M);
-    for (int o = 1; o < 64; o *= 2) L += __shfl_xor(L, o);
+__device__ __forceinline__ void join_stats(const f2 *st, int n, int stride, int lane, float &M, float &L) {
+    f2 mine = {-INFINITY, 0.0f};             // (a lane's own parts first)
+    for (int i = lane; i < n; i += 64) {
+        const f2 x = st[(int64_t)i * stride];
+        const float top = fmaxf(mine[0], x[0]);
+        if (top == -INFINITY) continue;
+        mine = f2{top, mine[1] * __builtin_amdgcn_exp2f(mine[0] - top) + x[1] * __builtin_amdgcn_exp2f(x[0] - top)};
+    }
+    M = wave_max(mine[0]);
+    L = wave_sum(mine[0] == -INFINITY ? 0.0f : mine[1] * __builtin_amdgcn_exp2f(mine[0] - M));
 }
 
 constexpr int kJoin = 256;     // threads of a joining workgroup
@@ -557,26 +579,26 @@ __global__ void __launch_bounds__(kJoin) join_kernel(Args a, int outs) {
     __shared__ float s_m[64], s_i[64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, D = a.c.D;
     const int rows_of_seq = a.c.heads * a.tiles;
-    const int64_t per = a.first[a.c.batch];
     // parts of head g of key-value head h of sequence b: their number, and the first
-    auto parts = [&](int b, int steps, int h, int g, int64_t &part) {
-        const int r = h * a.tiles + g / 16;
-        const int64_t u = a.first[b] * rows_of_seq + (int64_t)r * steps, w0 = u / per;
-        part = (w0 + (int64_t)b * rows_of_seq + r) * a.tile_heads + g % 16;
-        return steps ? (int)((u + steps - 1) / per - w0) + 1 : 0;
+    auto parts = [&](int b, int len, int h, int g, int64_t &part) {
+        const int64_t row = (int64_t)b * rows_of_seq + h * a.tiles + g / 16;
+        const int32_t w0 = a.ends[row * 2], w1 = a.ends[row * 2 + 1];   // (garbage in an empty row)
+        part = len > 0 ? (w0 + row) * a.tile_heads + g % 16 : 0;
+        return len > 0 ? w1 - w0 + 1 : 0;
     };
     if ((int)blockIdx.x < outs) {
         const int64_t head = (int64_t)blockIdx.x * HEADS + threadIdx.x / TPH;
         if (head >= (int64_t)a.c.batch * a.hq) return;   // (whole waves; with TPH = kJoin none)
         const int b = (int)(head / a.hq), i = (int)(head - (int64_t)b * a.hq), t = threadIdx.x % TPH;
         int64_t part;
-        const int n = parts(b, steps_of(a, length_of(a, b)), i / a.G, i % a.G, part);
-        const float *st = a.stat + part * 2, *po = a.part + part * D;
-        const int stride = a.tile_heads * 2;
+        const int n = parts(b, length_of(a, b), i / a.G, i % a.G, part);
+        const f2 *st = reinterpret_cast<const f2 *>(a.stat) + part;
+        const float *po = a.part + part * D;
+        const int stride = a.tile_heads;
         float M, L;
         join_stats(st, n, stride, lane, M, L);
         auto factor = [&](int s) {
-            const float m = st[(int64_t)s * stride];
+            const float m = st[(int64_t)s * stride][0];
             return m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - M);
         };
         f4 r = {0, 0, 0, 0};
@@ -629,9 +651,9 @@ __global__ void __launch_bounds__(kJoin) join_kernel(Args a, int outs) {
         if (g0) __syncthreads();
         for (int g = wave; g < gn; g += kJoin / 64) {
             int64_t part;
-            const int n = parts(b, steps_of(a, len), h, g0 + g, part);
+            const int n = parts(b, len, h, g0 + g, part);
             float M, L;
-            join_stats(a.stat + part * 2, n, a.tile_heads * 2, lane, M, L);
+            join_stats(reinterpret_cast<const f2 *>(a.stat) + part, n, a.tile_heads, lane, M, L);
             if (lane == 0) {
                 s_m[g] = M == -INFINITY ? 0.0f : M;
                 s_i[g] = M == -INFINITY ? 0.0f : 1.0f / L;
@@ -672,7 +694,7 @@ constexpr int kGroupsPerCu = 3;
 struct Plan {
     bool direct;
     int tiles, tile_heads, groups, score_ld;
-    size_t part, stat, first, scores;   // bytes
+    size_t part, stat, ends, scores;   // bytes
 };
 Plan plan_of(const rq_kv_cache *c, int q_heads, int64_t max_len, int track) {
     Plan p{};
@@ -690,7 +712,7 @@ Plan plan_of(const rq_kv_cache *c, int q_heads, int64_t max_len, int track) {
     const size_t parts = (size_t)(p.groups + rows) * p.tile_heads;
     p.part = round(parts * c->head_dim * 4);
     p.stat = round(parts * 8);
-    p.first = round(((size_t)c->batch + 1) * 8);
+    p.ends = round((size_t)rows * 8);
     p.scores = track ? round((size_t)rows * p.tile_heads * p.score_ld * 4) : 0;
     return p;
 }
@@ -699,7 +721,7 @@ Plan plan_of(const rq_kv_cache *c, int q_heads, int64_t max_len, int track) {
 
 size_t attend_workspace_bytes(const rq_kv_cache *c, int q_heads, int64_t max_len, int track) {
     const Plan p = plan_of(c, q_heads, max_len, track);
-    return p.part + p.stat + p.first + p.scores;
+    return p.part + p.stat + p.ends + p.scores;
 }
 
 int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_t q_ld, int q_heads,
@@ -714,8 +736,8 @@ int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_
     char *ws = static_cast<char *>(workspace);
     a.part = reinterpret_cast<float *>(ws);
     a.stat = reinterpret_cast<float *>(ws + p.part);
-    a.first = reinterpret_cast<int64_t *>(ws + p.part + p.stat);
-    a.scores = reinterpret_cast<float *>(ws + p.part + p.stat + p.first);
+    a.ends = reinterpret_cast<int32_t *>(ws + p.part + p.stat);
+    a.scores = reinterpret_cast<float *>(ws + p.part + p.stat + p.ends);
     a.q_ld = q_ld, a.out_ld = out_ld, a.mask_ld = mask_ld;
     a.hq = q_heads, a.G = q_heads / c->heads, a.tiles = p.tiles, a.tile_heads = p.tile_heads;
     a.max_len = (int)max_len, a.score_ld = p.score_ld, a.step_log = ilog2(step_of(c->head_dim > 128 ? 256 : c->head_dim > 64 ? 128 : 64, c->dtype == RQ_I8, bf16, p.direct));
