@@ -85,6 +85,8 @@ __device__ __forceinline__ u4 widen8(u2 c) {
     const u2 a = widen4(c[0]), b = widen4(c[1]);
     return u4{a[0], a[1], b[0], b[1]};
 }
+// an offset past any row of scores (2^30 bytes), whose end does not wrap either
+constexpr int kNowhere = 0x7ffffff0;
 constexpr float kLn2 = 0.69314718055994531f;
 template <bool BF16>
 __device__ __forceinline__ void store4(void *p, int64_t at, f4 v) {
@@ -224,6 +226,11 @@ __global__ void __launch_bounds__(waves_of(DIRECT) * 64) __attribute__((amdgpu_w
     };
     load_pages(0);
 
+    // this row's scores, as a buffer
+    const __amdgpu_buffer_rsrc_t score_row = __builtin_amdgcn_make_buffer_rsrc(
+        TRACK ? a.scores + ((int64_t)b * rows_of_seq + r) * a.score_ld * a.tile_heads : nullptr, 0,
+        TRACK ? a.score_ld * a.tile_heads * 4 : 0, 0x00020000);
+    const int score_lane = col < heads ? (col * 16 + g4 * 4) * 4 : kNowhere;
     // queries: piece s of lane (head, g4) holds d_of(s) .. + 7
     auto d_of = [&](int s) { return I8 && EXACT ? (s >> 1) * 64 + g4 * 16 + (s & 1) * 8 : s * 32 + g4 * 8; };
     u4 q[QP][KS];
@@ -258,7 +265,6 @@ __global__ void __launch_bounds__(waves_of(DIRECT) * 64) __attribute__((amdgpu_w
     float m = -INFINITY, l = 0.0f;
 
     constexpr int EB = I8 ? 1 : 2;   // bytes of an element
-    const int steps = here;
     const int page_mask = (1 << a.c.page_log) - 1;
 
     // base row of block x of a step; `there`: whether it has a page
@@ -273,71 +279,87 @@ __global__ void __launch_bounds__(waves_of(DIRECT) * 64) __attribute__((amdgpu_w
     u4 vreg[H * 4][NU];   // bf16: W / 2 dwords used; int8: W / 4
     f4 ks[H], vs[H];
     bool there[H];
+    uint32_t mreg[H];     // mask bytes of the lane's four tokens
 
-    auto load_k = [&](int step) {
+    // Loads of a later step leave under no condition, so that the compiler's count
+    // of what is in flight is exact and each use waits for its own operands only.
+    // Past the end (live is false) all lanes read one place of page 0.
+    const uint32_t k_lane = (col * D + (I8 && EXACT ? g4 * 16 : g4 * 8)) * EB;
+    const uint32_t v_lane = (g4 * 4 * D + ((EXACT || W * col < D) ? W * col : 0)) * EB;
+    auto load_k = [&](int step, int hf, bool live) {
+        const int64_t row = row_of(step, hf, there[hf]);
+        const char *base = static_cast<const char *>(a.c.k) + row * (D * EB);
+        const uint32_t lane_at = live ? k_lane : 0;
 #pragma unroll
-        for (int hf = 0; hf < H; ++hf) {
-            const int64_t row = row_of(step, hf, there[hf]);
-            const char *base = static_cast<const char *>(a.c.k) + row * (D * EB);
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                const int d = d_of(s);
-                const char *p = base + col * (D * EB) + d * EB;
-                if constexpr (!I8) {
-                    if (EXACT || d < D) kreg[hf][s] = *reinterpret_cast<const u4 *>(p);
-                    else kreg[hf][s] = u4{0, 0, 0, 0};
-                } else if constexpr (EXACT) {
-                    if (s % 2 == 0) kreg[hf][s / 2] = *reinterpret_cast<const u4 *>(p);
-                } else {
-                    u2 c = {0, 0};
-                    if (d < D) c = *reinterpret_cast<const u2 *>(p);
+        for (int s = 0; s < KS; ++s) {
+            if constexpr (I8 && EXACT) {
+                if (s % 2 == 0) kreg[hf][s / 2] = *reinterpret_cast<const u4 *>(base + lane_at + s * 32);
+            } else {
+                // (pieces past D: any place of the row; they are cleared where they are used)
+                const char *p = base + ((EXACT || d_of(s) < D) ? lane_at + s * 32 * EB : 0);
+                if constexpr (!I8) kreg[hf][s] = *reinterpret_cast<const u4 *>(p);
+                else {
+                    const u2 c = *reinterpret_cast<const u2 *>(p);
                     kreg[hf][s][0] = c[0];
                     kreg[hf][s][1] = c[1];
                 }
             }
-            if constexpr (I8) ks[hf] = *reinterpret_cast<const f4 *>(a.c.k_scale + row + g4 * 4);
+        }
+        if constexpr (I8) ks[hf] = *reinterpret_cast<const f4 *>(a.c.k_scale + row + (live ? g4 * 4 : 0));
+        if constexpr (MASKED) {
+            const uint8_t *mask = a.mask + (int64_t)b * a.mask_ld;
+            const int j = begin + (step * kWaves + wave) * TILE + hf * 16 + g4 * 4;
+            mreg[hf] = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mreg[hf] |= (uint32_t)(mask[min(j + i, end - 1)] != 0) << i;
         }
     };
-    auto load_v = [&](int step) {
+    auto load_v = [&](int step, int hf, bool live) {
+        bool unused;
+        const int64_t row = row_of(step, hf, unused);
+        const char *base = static_cast<const char *>(a.c.v) + row * (D * EB);
+        const uint32_t lane_at = live ? v_lane : 0;
 #pragma unroll
-        for (int hf = 0; hf < H; ++hf) {
-            bool unused;
-            const int64_t row = row_of(step, hf, unused);
-            const char *base = static_cast<const char *>(a.c.v) + row * (D * EB);
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int u = 0; u < NU; ++u) {
-                    int d = W * col + 16 * W * u;
-                    if (!EXACT && d >= D) d = 0;   // (columns of the product that nobody reads)
-                    const char *p = base + (g4 * 4 + i) * (D * EB) + d * EB;
-                    u4 &r = vreg[hf * 4 + i][u];
-                    if constexpr (W * EB == 16) r = *reinterpret_cast<const u4 *>(p);
-                    else if constexpr (W * EB == 8) {
-                        const u2 x = *reinterpret_cast<const u2 *>(p);
-                        r[0] = x[0];
-                        r[1] = x[1];
-                    } else r[0] = *reinterpret_cast<const uint32_t *>(p);
-                }
-            if constexpr (I8) vs[hf] = *reinterpret_cast<const f4 *>(a.c.v_scale + row + g4 * 4);
-        }
+            for (int u = 0; u < NU; ++u) {
+                // (d past D: columns of the product that nobody reads)
+                const char *p = base + lane_at + ((EXACT || u == 0 || W * col + 16 * W * u < D) ? i * D + 16 * W * u : 0) * EB;
+                u4 &r = vreg[hf * 4 + i][u];
+                if constexpr (W * EB == 16) r = *reinterpret_cast<const u4 *>(p);
+                else if constexpr (W * EB == 8) {
+                    const u2 x = *reinterpret_cast<const u2 *>(p);
+                    r[0] = x[0];
+                    r[1] = x[1];
+                } else r[0] = *reinterpret_cast<const uint32_t *>(p);
+            }
+        if constexpr (I8) vs[hf] = *reinterpret_cast<const f4 *>(a.c.v_scale + row + (live ? g4 * 4 : 0));
     };
 
     auto mine = [&](int step) { return begin + (step * kWaves + wave) * TILE < end; };   // wave-uniform
     if (mine(0)) {
-        load_k(0);
-        load_v(0);
+#pragma unroll
+        for (int hf = 0; hf < H; ++hf) load_k(0, hf, true);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int hf = 0; hf < H; ++hf) load_v(0, hf, true);
+        __builtin_amdgcn_sched_barrier(0);
     }
-    for (int step = 0; step < steps && mine(step); ++step) {
+    for (int step = 0; mine(step); ++step) {
         const int j0 = begin + (step * kWaves + wave) * TILE;
-        const bool more = step + 1 < steps && mine(step + 1);
+        const bool more = mine(step + 1);
+        if (((step + 1) & (64 / H - 1)) == 0) {
+            load_pages(step + 1);
+            asm volatile("" : "+v"(page_of));   // waited for here and nowhere else
+        }
         // scores: lane (head col, g4) gets tokens j0 + 16 hf + 4 g4 + i
         f4 s[H];
         bool ok[H];
-#pragma unroll
-        for (int hf = 0; hf < H; ++hf) ok[hf] = there[hf];
+        uint32_t masked_in[H];
 #pragma unroll
         for (int hf = 0; hf < H; ++hf) {
+            ok[hf] = there[hf];
+            masked_in[hf] = MASKED ? mreg[hf] : 15;
             s[hf] = f4{0, 0, 0, 0};
 #pragma unroll
             for (int t = 0; t < KS; ++t) {
@@ -345,6 +367,7 @@ __global__ void __launch_bounds__(waves_of(DIRECT) * 64) __attribute__((amdgpu_w
                 if constexpr (!I8) k = kreg[hf][t];
                 else if constexpr (EXACT) k = widen8(t & 1 ? u2{kreg[hf][t / 2][2], kreg[hf][t / 2][3]} : u2{kreg[hf][t / 2][0], kreg[hf][t / 2][1]});
                 else k = widen8(u2{kreg[hf][t][0], kreg[hf][t][1]});
+                if (!EXACT && d_of(t) >= D) k = u4{0, 0, 0, 0};
 #pragma unroll
                 for (int p = 0; p < QP; ++p) s[hf] = mfma(k, q[p][t], s[hf]);
             }
@@ -353,11 +376,9 @@ __global__ void __launch_bounds__(waves_of(DIRECT) * 64) __attribute__((amdgpu_w
                 s[hf][i] *= a.scale2;
                 if constexpr (I8) s[hf][i] *= ks[hf][i];
             }
+            load_k(step + 1, hf, more);
         }
-        if (more) {
-            if (((step + 1) & (64 / H - 1)) == 0) load_pages(step + 1);
-            load_k(step + 1);
-        }
+        __builtin_amdgcn_sched_barrier(0);
         // tokens that are left out
         bool whole = j0 + TILE <= end && !MASKED;
 #pragma unroll
@@ -369,18 +390,21 @@ __global__ void __launch_bounds__(waves_of(DIRECT) * 64) __attribute__((amdgpu_w
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int j = j0 + hf * 16 + g4 * 4 + i;
-                    use[hf][i] = ok[hf] && j < end;
-                    if constexpr (MASKED) {
-                        if (use[hf][i]) use[hf][i] = a.mask[(int64_t)b * a.mask_ld + j] != 0;
-                    }
-                    if (!use[hf][i]) s[hf][i] = -INFINITY;
+                    // (one expression without branches: taken apart into nested ones by &&,
+                    // the store into the vector's element was lost for masked tokens)
+                    const bool in = (int)ok[hf] & (int)(j < end) & (int)(masked_in[hf] >> i & 1);
+                    const float x = s[hf][i];
+                    s[hf][i] = in ? x : -INFINITY;
+                    use[hf][i] = in;
                 }
         }
         if constexpr (TRACK) {
-            if (col < heads)
+            // (a buffer store drops the lanes whose offset lies past the row; under a
+            // branch the count of what is in flight would not be exact any more)
 #pragma unroll
-                for (int hf = 0; hf < H; ++hf)
-                    *reinterpret_cast<f4 *>(a.scores + (((int64_t)b * rows_of_seq + r) * a.score_ld + j0 + hf * 16) * a.tile_heads + col * 16 + g4 * 4) = s[hf];
+            for (int hf = 0; hf < H; ++hf)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, s[hf]), score_row, score_lane,
+                                                       (j0 + hf * 16) * a.tile_heads * 4, 0);
         }
         // The running maximum only moves when a score passes it by 2^8: weights
         // up to 256 are as exact, and most steps leave the sums as they are.
@@ -457,8 +481,10 @@ __global__ void __launch_bounds__(waves_of(DIRECT) * 64) __attribute__((amdgpu_w
                     }
                 }
             }
+            load_v(step + 1, 2 * y2, more);
+            load_v(step + 1, 2 * y2 + 1, more);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (more) load_v(step + 1);
     }
 
     // join the waves: o of lane (head col, g4) is d = W (4 g4 + i) + 16 W u + j
