@@ -714,8 +714,8 @@ __global__ void __launch_bounds__(kJoin) join_kernel(Args a, int outs) {
 // 350 us (6.0 TB/s) against 376, uneven 195 against 217; 128 of 4000, uneven 204
 // against 203; but 64 of up to 8000, uneven 221 against 197.
 constexpr int kDirect = 512;
-// Shares per CU otherwise: what is resident at once of the commonest variant
-// (2 and 4 were within 3% for 131071 tokens and for batches).
+// Shares per CU otherwise, at most: what is resident of the variant with the
+// fewest registers.
 constexpr int kGroupsPerCu = 3;
 struct Plan {
     bool direct;
@@ -755,6 +755,10 @@ int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_
                            int64_t mask_ld, void *out, int64_t out_ld, float *lse, int track,
                            float *weight_out, void *workspace, void *stream) {
     const Plan p = plan_of(c, q_heads, max_len, track);
+    // as many shares as are resident at once
+    const int DP = c->head_dim > 128 ? 256 : c->head_dim > 64 ? 128 : 64;
+    const int fit = device_cus() * std::min(kGroupsPerCu, resident(DP, c->head_dim == DP, bf16, c->dtype == RQ_I8));
+    const unsigned groups = p.direct ? (unsigned)c->batch * c->heads * p.tiles : (unsigned)std::min(p.groups, fit);
     Args a{};
     a.c = device_cache(c);
     a.q = q, a.out = out, a.lens = lens, a.mask = mask, a.lse = lse;
@@ -766,10 +770,9 @@ int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_
     a.scores = reinterpret_cast<float *>(ws + p.part + p.stat + p.ends);
     a.q_ld = q_ld, a.out_ld = out_ld, a.mask_ld = mask_ld;
     a.hq = q_heads, a.G = q_heads / c->heads, a.tiles = p.tiles, a.tile_heads = p.tile_heads;
-    a.max_len = (int)max_len, a.score_ld = p.score_ld, a.step_log = ilog2(step_of(c->head_dim > 128 ? 256 : c->head_dim > 64 ? 128 : 64, c->dtype == RQ_I8, bf16, p.direct));
+    a.max_len = (int)max_len, a.score_ld = p.score_ld, a.step_log = ilog2(step_of(DP, c->dtype == RQ_I8, bf16, p.direct));
     a.scale2 = scale * 1.4426950408889634f;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const unsigned groups = p.direct ? (unsigned)c->batch * c->heads * p.tiles : (unsigned)p.groups;
     auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(groups), dim3(waves_of(p.direct) * 64), 0, s, a); };
     auto pick = [&](auto dp, auto exact, auto i8, auto io) {
         constexpr int DP = decltype(dp)::value;
