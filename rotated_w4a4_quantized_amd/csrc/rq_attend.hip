@@ -2,9 +2,15 @@
 //
 //   s_j = scale q . k_j;  lse = log sum exp s_j;  out = sum exp(s_j - lse) v_j
 //
-// The cache is read once and nothing else is large, so HBM bounds it.  The
-// tokens of all sequences are dealt out to the workgroups in equal shares, and
-// a second kernel joins the parts of rows; short calls take one workgroup a row.
+// The cache is read once and nothing else is large, so HBM bounds it: 131071
+// tokens of 8 heads x 128 in bf16 (537 MB) take 94 us, 5.7 TB/s, where a plain
+// read of as much takes 87 us; 262143 tokens in int8 103 us, 5.4 TB/s.  The
+// matrix cores are 5% busy; they are there because 4 to 16 query heads a key
+// would keep the vector units too busy to issue the loads.
+//
+// The tokens of all sequences are dealt out to the workgroups in equal shares, and
+// a second kernel joins the parts of rows (7 us for 131071 tokens); short calls, and
+// calls of many short rows, take one workgroup a row and no second kernel.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -209,7 +215,7 @@ __global__ void __launch_bounds__(waves_of(DIRECT) * 64) __attribute__((amdgpu_w
         step0 = __builtin_amdgcn_readfirstlane((int)(off - (int64_t)r * n));
     }
 
-    for (;;) {   // (rows of this workgroup; the body keeps its indentation)
+    for (;;) {   // (rows of this workgroup's share)
     const int row_steps = steps_of(a, len);
     const int here = DIRECT ? row_steps : (int)min((int64_t)(row_steps - step0), u_end - u);
     const int begin = step0 * STEP, end = min(len, begin + here * STEP);
@@ -591,7 +597,8 @@ __device__ __forceinline__ void join_stats(const f2 *st, int n, int stride, int 
 
 constexpr int kJoin = 256;     // threads of a joining workgroup
 
-// Joins the parts of rows.  The first outs workgroups write outputs, a head by
+// Joins the parts of rows (5 to 7 us; with the weights of 64 sequences of 4000
+// tokens 18 us, 50 MB).  The first outs workgroups write outputs, a head by
 // TPH threads each (all of a workgroup where heads are few, a wave where there
 // are many); the others add the weights of kJoin * 4 slots of one key-value
 // head.  All parts' factors come first, so that the loads of the partial outputs
