@@ -766,6 +766,13 @@ int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_
     const int DP = c->head_dim > 128 ? 256 : c->head_dim > 64 ? 128 : 64;
     const int fit = device_cus() * std::min(kGroupsPerCu, resident(DP, c->head_dim == DP, bf16, c->dtype == RQ_I8));
     const unsigned groups = p.direct ? (unsigned)c->batch * c->heads * p.tiles : (unsigned)std::min(p.groups, fit);
+    const int64_t heads = (int64_t)c->batch * q_heads;
+    const int64_t weights = track ? (max_len + kJoin * 4 - 1) / (kJoin * 4) * c->batch * c->heads : 0;
+    // a wave a head once that fills the device
+    const bool many = heads >= 4 * device_cus();
+    const int64_t outs = many ? (heads + kJoin / 64 - 1) / (kJoin / 64) : heads;
+    // (workgroups of 256: a launch holds 2^24 of them)
+    if (!p.direct && outs + weights >= (1 << 24)) return (int)hipErrorInvalidValue;
     Args a{};
     a.c = device_cache(c);
     a.q = q, a.out = out, a.lens = lens, a.mask = mask, a.lse = lse;
@@ -810,13 +817,6 @@ int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_
     else if (c->head_dim <= 128) dims(std::integral_constant<int, 128>{});
     else dims(std::integral_constant<int, 256>{});
     if (!p.direct) {
-        const int64_t heads = (int64_t)c->batch * q_heads;
-        const int64_t weights = track ? (max_len + kJoin * 4 - 1) / (kJoin * 4) * c->batch * c->heads : 0;
-        // a wave a head once that fills the device
-        const bool many = heads >= 4 * device_cus();
-        const int64_t outs = many ? (heads + kJoin / 64 - 1) / (kJoin / 64) : heads;
-        // (workgroups of 256: a launch holds 2^24 of them)
-        if (outs + weights >= (1 << 24)) return (int)hipErrorInvalidValue;
         auto join = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((unsigned)(outs + weights)), dim3(kJoin), 0, s, a, (int)outs); };
         if (bf16) many ? join(join_kernel<true, 64>) : join(join_kernel<true, kJoin>);
         else many ? join(join_kernel<false, 64>) : join(join_kernel<false, kJoin>);

@@ -61,6 +61,7 @@ NORM = [
     (2500, 24, 24, 128, 128, True, "bf16", None, 16),
     (2500, 20, 4, 64, 0, False, "f32", "bf16", 64),
     (4099, 1, 1, 40, 16, False, "bf16", "int8", 16),
+    (20001, 2, 1, 64, 64, True, "bf16", "bf16", 64),      # more tokens than waves: each walks over several
 ]
 
 
@@ -310,6 +311,37 @@ def test_paged_attention(B, hq, hkv, D, page, lens, dtype, kind, mode):
                  cache.weight if mode == "track" else None)
 
 
+@pytest.mark.parametrize("B,hkv,top,track,dtype,kind", [
+    (130, 2, 1500, False, "bf16", "bf16"),     # shares that span rows and end inside them
+    (130, 2, 1500, True, "f32", "bf16"),
+    (300, 4, 700, True, "bf16", "int8"),       # several rows, and empty sequences, in a share
+    (300, 4, 700, False, "bf16", "bf16"),      # many rows: one workgroup each
+    (70, 4, 1100, False, "f32", "int8"),
+])
+def test_paged_attention_many_uneven_rows(B, hkv, top, track, dtype, kind):
+    rng = np.random.default_rng(B + top)
+    D, page = 64, 16
+    lens = (rng.integers(1, top + 1, B) * (rng.random(B) < 0.7)).tolist()
+    lens[0], lens[1], lens[-1] = 0, top, 0
+    cache, k, v, table, weight = build(rng, B, hkv, D, page, lens, kind, track)
+    q, qx = rand(rng, (B, 2 * hkv * D), dtype, 2.0)
+    out, lse = run_attend(cache, q, torch.tensor(lens, dtype=torch.int32, device="cuda"), top, None, track)
+    check_attend(cache, k, v, table, weight, q, qx, lens, top, None, D ** -0.5, out, lse, dtype, cache.weight if track else None)
+
+
+def test_paged_attention_without_tokens():
+    """No sequence has a token, by length or by max_len 0."""
+    rng = np.random.default_rng(17)
+    for track in (False, True):
+        for max_len, lens in ((0, [5, 9]), (600, [0, 0]), (100, [0, -3])):
+            cache, *_ = build(rng, 2, 2, 64, 16, [600, 600], "bf16", track)
+            before = None if cache.weight is None else cache.weight.clone()
+            q, _ = rand(rng, (2, 4 * 64), "bf16")
+            out, lse = run_attend(cache, q, torch.tensor(lens, dtype=torch.int32, device="cuda"), max_len, None, track)
+            assert (out == 0).all() and (lse == -float("inf")).all()
+            assert before is None or same_bits(before, cache.weight)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "int8"])
 def test_paged_attention_values_in_masked_places(kind):
     """NaN and infinities where the mask leaves out, in keys and in values."""
@@ -502,6 +534,26 @@ def test_cache_evict(B, hkv, D, page, lens, keep, recent, sink, kind, what, in_p
     if not in_place:
         assert np.array_equal(cache.weight.cpu().numpy().view(np.int32), weight.view(np.int32))
         assert np.array_equal(cache.pos.cpu().numpy(), pos) and tl.cpu().tolist() == lens
+
+
+@pytest.mark.parametrize("n", [3000, 40000])
+@pytest.mark.parametrize("apart", ["weight", "pos", "lens"])
+def test_cache_evict_some_outputs_in_place(n, apart):
+    rng = np.random.default_rng(n)
+    hkv, D, page, keep, recent = 2, 16, 64, n // 3, 50
+    base, _, _, table, _ = build(rng, 1, hkv, D, page, [n], "bf16", False, junk=False)
+    meta = (1, hkv, base.slots)
+    weight, pos = rng.uniform(0, 1, meta).astype(np.float32), np.stack([rng.permutation(base.slots) for _ in range(hkv)])[None].astype(np.int32)
+    cache = rq.KVCache(base.k, base.v, base.table, weight=torch.from_numpy(weight.copy()).cuda(), pos=torch.from_numpy(pos.copy()).cuda())
+    tl = torch.tensor([n], dtype=torch.int32, device="cuda")
+    outs = {"weight": dict(weight_out=torch.zeros_like(cache.weight)), "pos": dict(pos_out=torch.zeros_like(cache.pos)),
+            "lens": dict(lens_out=torch.zeros_like(tl))}[apart]
+    rq.cache_evict(cache, tl, keep, recent=recent, max_len=n, workspace=torch.empty(rq.cache_evict_workspace_bytes(cache, keep, n), dtype=torch.uint8, device="cuda"), **outs)
+    got_w, got_p = outs.get("weight_out", cache.weight).cpu().numpy(), outs.get("pos_out", cache.pos).cpu().numpy()
+    assert outs.get("lens_out", tl).item() == keep
+    for h in range(hkv):
+        _, come = A.evict_row(weight[0, h], pos[0, h], n, keep, recent, 0)
+        assert np.array_equal(got_w[0, h, :keep], weight[0, h, come]) and np.array_equal(got_p[0, h, :keep], pos[0, h, come])
 
 
 def test_cache_evict_keeps_attention_of_survivors():
