@@ -94,17 +94,20 @@ __device__ void copy_moves(const Args &a, int b, int h, const int32_t *free_list
     const int t = threadIdx.x;
     for (int at = first; at < last; at += ROWS) {
         const int n = min(ROWS, last - at);
+        bool scaled = false;
         if (t < n) {
             const int64_t to = a.c.row(b, h, free_list[at + t]), from = a.c.row(b, h, up_list[at + t]);
             const bool both = to >= 0 && from >= 0;
             s_rows[0][t] = both ? to : -1;
             s_rows[1][t] = from;
-            if (both && a.c.k_scale) {
-                a.c.k_scale[to] = a.c.k_scale[from];
-                a.c.v_scale[to] = a.c.v_scale[from];
-            }
+            scaled = both && a.c.k_scale;
         }
         __syncthreads();
+        float ks = 0.0f, vs = 0.0f;      // (asked for after the barrier, which would wait for them)
+        if (scaled) {
+            ks = a.c.k_scale[s_rows[1][t]];
+            vs = a.c.v_scale[s_rows[1][t]];
+        }
         const int vecs = a.row_bytes / VEC, all = n * vecs * 2;
         for (int i0 = t; i0 < all; i0 += THREADS * U) {
             u4 x[U];
@@ -133,6 +136,10 @@ __device__ void copy_moves(const Args &a, int b, int h, const int32_t *free_list
                     if constexpr (VEC == 16) *reinterpret_cast<u4 *>(to[u]) = x[u];
                     else *reinterpret_cast<u2 *>(to[u]) = u2{x[u][0], x[u][1]};
                 }
+        }
+        if (scaled) {
+            a.c.k_scale[s_rows[0][t]] = ks;
+            a.c.v_scale[s_rows[0][t]] = vs;
         }
         __syncthreads();
     }
