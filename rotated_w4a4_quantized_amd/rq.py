@@ -532,15 +532,21 @@ def _io_dtype(t) -> int:
 def _rows(t, n, width, name):
     """Address and row stride of a 2-D (or [n][heads][D]) tensor of n rows of
     width elements, each row contiguous."""
-    if t.dim() == 3:
-        if t.shape[1] * t.shape[2] != width or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-            raise ValueError(f"{name} must be rows of {width} contiguous elements")
-    elif t.dim() != 2 or t.shape[1] < width or (width > 1 and t.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        have = shape[1]
+        ok = have >= width and (stride[1] == 1 or width == 1)
+    elif len(shape) == 3:
+        have = shape[1] * shape[2]
+        ok = have == width and stride[2] == 1 and (stride[1] == shape[2] or shape[1] == 1)
+    else:
+        ok = False
+    if not ok:
         raise ValueError(f"{name} must be rows of {width} contiguous elements")
-    if t.shape[0] != n:
-        raise ValueError(f"{name} must have {n} rows, got {t.shape[0]}")
+    if shape[0] != n:
+        raise ValueError(f"{name} must have {n} rows, got {shape[0]}")
     # (a single row has no stride to keep to)
-    return t.data_ptr(), t.stride(0) if n > 1 else max(width, t.shape[1] if t.dim() == 2 else width)
+    return t.data_ptr(), stride[0] if n > 1 else have
 
 
 def _vector(t, n, dtype, name):
