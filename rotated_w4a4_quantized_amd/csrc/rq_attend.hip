@@ -51,21 +51,21 @@ struct Args {
 };
 
 // Waves of a workgroup: 4, and 8 in a direct call, which has one workgroup a row
-// and wants it done soon.
-constexpr int waves_of(bool direct) { return direct ? 8 : 4; }
+// and wants it done soon (D > 128 needs the registers of 4).
+constexpr int waves_of(int DP, bool direct) { return direct && DP <= 128 ? 8 : 4; }
 // 16-token blocks of one wave's step: 16 KB of keys and values of 128 dimensions
 // are in flight per wave for either type.  (int8 steps of 2 blocks took 5% longer
 // on 48 sequences of 4096 tokens; fp32 queries and D > 128 leave no registers for
 // 4.)
 constexpr int blocks_of(int DP, bool i8, bool bf16) { return i8 && bf16 && DP <= 128 ? 4 : 2; }
 // tokens of one workgroup's step
-constexpr int step_of(int DP, bool i8, bool bf16, bool direct) { return waves_of(direct) * 16 * blocks_of(DP, i8, bf16); }
-constexpr int kLeastStep = waves_of(false) * 32;
+constexpr int step_of(int DP, bool i8, bool bf16, bool direct) { return waves_of(DP, direct) * 16 * blocks_of(DP, i8, bf16); }
+constexpr int kLeastStep = waves_of(128, false) * 32;
 constexpr int kMaxGroups = 1024;   // workgroups of a divided call, at most
 
 // waves of a SIMD, by the registers they need
-constexpr int resident(int DP, bool exact, bool bf16, bool i8) {
-    return DP == 256 ? 1 : DP == 128 ? (exact && bf16 && !i8 ? 3 : 2) : (bf16 && i8 ? 2 : 3);
+constexpr int resident(int DP, bool plain, bool bf16, bool i8) {   // plain: D == DP and no mask
+    return DP == 256 ? 1 : DP == 128 ? (plain && bf16 && !i8 ? 3 : 2) : (bf16 && i8 ? 2 : 3);
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -148,13 +148,13 @@ __device__ __forceinline__ int steps_of(const Args &a, int len) { return (int)((
 // and three for fp32: with one part their rounding would be as large as the
 // output's own.  Sums and statistics are fp32.
 template <int DP, bool EXACT, bool I8, bool BF16, bool MASKED, bool TRACK, bool DIRECT>
-__global__ void __launch_bounds__(waves_of(DIRECT) * 64) __attribute__((amdgpu_waves_per_eu(DIRECT ? 1 : resident(DP, EXACT, BF16, I8)))) attend_kernel(Args a) {
+__global__ void __launch_bounds__(waves_of(DP, DIRECT) * 64) __attribute__((amdgpu_waves_per_eu(DIRECT ? 1 : resident(DP, EXACT && !MASKED, BF16, I8)))) attend_kernel(Args a) {
     constexpr int QP = BF16 ? 1 : 3, PP = BF16 ? 2 : 3;
     constexpr int KS = DP / 32;                  // products along d
     constexpr int W = DP == 64 ? 4 : 8;          // d of one value load
     constexpr int NU = DP / (16 * W);            // value loads of a token
     constexpr int H = blocks_of(DP, I8, BF16), TILE = 16 * H, STEP = step_of(DP, I8, BF16, DIRECT);
-    constexpr int kWaves = waves_of(DIRECT), kThreads = kWaves * 64;
+    constexpr int kWaves = waves_of(DP, DIRECT), kThreads = kWaves * 64;
     __shared__ float s_m[kWaves][16], s_l[kWaves][16];
     __shared__ float s_o[kWaves][16][DP + 4];
 
@@ -540,6 +540,38 @@ __global__ void __launch_bounds__(waves_of(DIRECT) * 64) __attribute__((amdgpu_w
             if (d == 0 && a.lse) a.lse[head0 + g] = mm == -INFINITY ? -INFINITY : (mm + log2f(ll)) * kLn2;
         }
     }
+    if constexpr (DIRECT && TRACK) {
+        // this workgroup has all heads of its key-value head (one tile) and all their
+        // scores: it adds the weights up itself
+        __shared__ float s_fin[2][16];
+        if ((int)threadIdx.x < heads) {
+            float mm = -INFINITY, ll = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, s_m[w][threadIdx.x]);
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w)
+                if (s_m[w][threadIdx.x] != -INFINITY) ll += s_l[w][threadIdx.x] * __builtin_amdgcn_exp2f(s_m[w][threadIdx.x] - mm);
+            s_fin[0][threadIdx.x] = mm == -INFINITY ? 0.0f : mm;
+            s_fin[1][threadIdx.x] = mm == -INFINITY ? 0.0f : 1.0f / ll;
+        }
+        __threadfence_block();
+        __syncthreads();
+        const int64_t row = (int64_t)b * rows_of_seq + r;
+        for (int j = threadIdx.x * 4; j < len; j += kThreads * 4) {
+            const float *sc = a.scores + (row * a.score_ld + (j & ~15)) * a.tile_heads + (j & 15);
+            const int64_t at = row * a.c.slots() + j;
+            const f4 before = *reinterpret_cast<const f4 *>(a.weight + at);   // (slots come in whole pages)
+            f4 add = {0, 0, 0, 0};
+#pragma unroll 4
+            for (int g = 0; g < heads; ++g) {
+                const f4 x = *reinterpret_cast<const f4 *>(sc + g * 16);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) add[e] += __builtin_amdgcn_exp2f(x[e] - s_fin[0][g]) * s_fin[1][g];
+            }
+            for (int e = 0; e < 4; ++e)
+                if (j + e < len) a.weight_out[at + e] = before[e] + add[e];
+        }
+    }
     if constexpr (DIRECT) return;
     if (threadIdx.x == 0) {
         int32_t *e = a.ends + ((int64_t)b * rows_of_seq + r) * 2;
@@ -735,18 +767,19 @@ Plan plan_of(const rq_kv_cache *c, int q_heads, int64_t max_len, int track) {
     p.tiles = (G + 15) / 16;
     p.tile_heads = std::min(G, 16);
     const int64_t rows = (int64_t)c->batch * c->heads * p.tiles;
-    p.direct = !track && rows <= (1 << 20) && (max_len <= kDirect || (rows >= device_cus() && max_len <= 4 * rows));
+    // (tracked: where the workgroup has all of a key-value head's query heads)
+    p.direct = (!track || p.tiles == 1) && rows <= (1 << 20) && (max_len <= kDirect || (rows >= device_cus() && max_len <= 4 * rows));
     p.score_ld = (int)((max_len + 63) / 64 * 64);   // whole steps of a wave are written
+    auto round = [](size_t n) { return (n + 15) / 16 * 16; };
+    p.scores = track ? round((size_t)rows * p.tile_heads * p.score_ld * 4) : 0;
     if (p.direct) return p;
     // (the least step, whatever the type of the queries: the workspace does not depend on it)
     const int64_t steps = rows * ((max_len + kLeastStep - 1) / kLeastStep);
     p.groups = (int)std::max<int64_t>(1, std::min<int64_t>({steps, (int64_t)device_cus() * kGroupsPerCu, kMaxGroups}));
-    auto round = [](size_t n) { return (n + 15) / 16 * 16; };
     const size_t parts = (size_t)(p.groups + rows) * p.tile_heads;
     p.part = round(parts * c->head_dim * 4);
     p.stat = round(parts * 8);
     p.ends = round((size_t)rows * 8);
-    p.scores = track ? round((size_t)rows * p.tile_heads * p.score_ld * 4) : 0;
     return p;
 }
 
@@ -764,7 +797,7 @@ int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_
     const Plan p = plan_of(c, q_heads, max_len, track);
     // as many shares as are resident at once
     const int DP = c->head_dim > 128 ? 256 : c->head_dim > 64 ? 128 : 64;
-    const int fit = device_cus() * std::min(kGroupsPerCu, resident(DP, c->head_dim == DP, bf16, c->dtype == RQ_I8));
+    const int fit = device_cus() * std::min(kGroupsPerCu, resident(DP, c->head_dim == DP && !mask, bf16, c->dtype == RQ_I8));
     const unsigned groups = p.direct ? (unsigned)c->batch * c->heads * p.tiles : (unsigned)std::min(p.groups, fit);
     const int64_t heads = (int64_t)c->batch * q_heads;
     const int64_t weights = track ? (max_len + kJoin * 4 - 1) / (kJoin * 4) * c->batch * c->heads : 0;
@@ -787,20 +820,19 @@ int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_
     a.max_len = (int)max_len, a.score_ld = p.score_ld, a.step_log = ilog2(step_of(DP, c->dtype == RQ_I8, bf16, p.direct));
     a.scale2 = scale * 1.4426950408889634f;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(groups), dim3(waves_of(p.direct) * 64), 0, s, a); };
+    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(groups), dim3(waves_of(DP, p.direct) * 64), 0, s, a); };
     auto pick = [&](auto dp, auto exact, auto i8, auto io) {
         constexpr int DP = decltype(dp)::value;
         constexpr bool E = decltype(exact)::value, I = decltype(i8)::value, B = decltype(io)::value;
-        if (p.direct) {
-            if (mask) go(attend_kernel<DP, E, I, B, true, false, true>);
-            else go(attend_kernel<DP, E, I, B, false, false, true>);
-        } else if (mask) {
-            if (track) go(attend_kernel<DP, E, I, B, true, true, false>);
-            else go(attend_kernel<DP, E, I, B, true, false, false>);
-        } else {
-            if (track) go(attend_kernel<DP, E, I, B, false, true, false>);
-            else go(attend_kernel<DP, E, I, B, false, false, false>);
-        }
+        auto run = [&](auto direct) {
+            constexpr bool R = decltype(direct)::value;
+            if (mask && track) go(attend_kernel<DP, E, I, B, true, true, R>);
+            else if (mask) go(attend_kernel<DP, E, I, B, true, false, R>);
+            else if (track) go(attend_kernel<DP, E, I, B, false, true, R>);
+            else go(attend_kernel<DP, E, I, B, false, false, R>);
+        };
+        if (p.direct) run(std::true_type{});
+        else run(std::false_type{});
     };
     auto types = [&](auto dp, auto exact) {
         const bool i8 = c->dtype == RQ_I8;
