@@ -3,9 +3,9 @@
 //   s_j = scale q . k_j;  lse = log sum exp s_j;  out = sum exp(s_j - lse) v_j
 //
 // The cache is read once and nothing else is large, so HBM bounds it: 131071
-// tokens of 8 heads x 128 in bf16 (537 MB) take 94 us, 5.7 TB/s, where a plain
-// read of as much takes 87 us; 262143 tokens in int8 103 us, 5.4 TB/s.  The
-// matrix cores are 5% busy; they are there because 4 to 16 query heads a key
+// tokens of 8 heads x 128 in bf16 (537 MB) take 95 us, 5.7 TB/s, where a plain
+// read of as much takes 87 us; 262143 tokens in int8 108 us with the joining, 5.1
+// TB/s.  The matrix cores are 5% busy; they are there because 4 to 16 query heads a key
 // would keep the vector units too busy to issue the loads.
 //
 // The tokens of all sequences are dealt out to the workgroups in equal shares, and
@@ -54,8 +54,8 @@ struct Args {
 // and wants it done soon (D > 128 needs the registers of 4).
 constexpr int waves_of(int DP, bool direct) { return direct && DP <= 128 ? 8 : 4; }
 // 16-token blocks of one wave's step: 16 KB of keys and values of 128 dimensions
-// are in flight per wave for either type.  (int8 steps of 2 blocks took 5% longer
-// on 48 sequences of 4096 tokens; fp32 queries and D > 128 leave no registers for
+// are in flight per wave for either type.  (int8 steps of 2 blocks took 3 to 5%
+// longer on 48 uneven sequences of up to 8190 tokens; fp32 queries and D > 128 leave no registers for
 // 4.)
 constexpr int blocks_of(int DP, bool i8, bool bf16) { return i8 && bf16 && DP <= 128 ? 4 : 2; }
 // tokens of one workgroup's step

@@ -267,8 +267,8 @@ int launch_qk_norm_rope(const rq_qk_norm *d, const void *qkv, int bf16, int64_t 
     const int64_t full = (int64_t)device_cus() * 16;
     a.per = (int)std::min<int64_t>(groups, std::max<int64_t>(1, (T * groups + full - 1) / full));
     a.chunks = (groups + a.per - 1) / a.per;
-    // Twice what is resident, then waves walk over visits: 32760 tokens of 24 heads
-    // take 87 us, one visit a wave 101 us, a single round of waves 91 us.
+    // Twice what is resident, then waves walk over visits: for 32760 tokens of 24
+    // heads that took 87 us (83 now), one visit a wave 101, a single round of waves 91.
     const int64_t wgs = std::min<int64_t>((T * a.chunks + 3) / 4, (int64_t)device_cus() * 8);
     auto go = [&](auto kern) {
         hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(256), 0, static_cast<hipStream_t>(stream), a);
