@@ -53,19 +53,18 @@ struct Args {
 // Waves of a workgroup: 4, and 8 in a direct call, which has one workgroup a row
 // and wants it done soon (D > 128 needs the registers of 4).
 constexpr int waves_of(int DP, bool direct) { return direct && DP <= 128 ? 8 : 4; }
-// 16-token blocks of one wave's step: 16 KB of keys and values of 128 dimensions
-// are in flight per wave for either type.  (int8 steps of 2 blocks took 3 to 5%
-// longer on 48 uneven sequences of up to 8190 tokens; fp32 queries and D > 128 leave no registers for
-// 4.)
-constexpr int blocks_of(int DP, bool i8, bool bf16) { return i8 && bf16 && DP <= 128 ? 4 : 2; }
+// 16-token blocks of one wave's step: the 32 tokens of one value product.  (4 for
+// int8, as many bytes as bf16, need the registers of a third wave: 48 uneven
+// sequences of up to 8190 tokens took 102 us against 86, 200 of 1000 78 against 60.)
+constexpr int kBlocks = 2, kTile = 16 * kBlocks;
 // tokens of one workgroup's step
-constexpr int step_of(int DP, bool i8, bool bf16, bool direct) { return waves_of(DP, direct) * 16 * blocks_of(DP, i8, bf16); }
-constexpr int kLeastStep = waves_of(128, false) * 32;
+constexpr int step_of(int DP, bool direct) { return waves_of(DP, direct) * kTile; }
+constexpr int kLeastStep = waves_of(128, false) * kTile;
 constexpr int kMaxGroups = 1024;   // workgroups of a divided call, at most
 
 // waves of a SIMD, by the registers they need
-constexpr int resident(int DP, bool plain, bool bf16, bool i8) {   // plain: D == DP and no mask
-    return DP == 256 ? 1 : DP == 128 ? (plain && bf16 && !i8 ? 3 : 2) : (bf16 && i8 ? 2 : 3);
+constexpr int resident(int DP, bool plain, bool bf16) {   // plain: D == DP and no mask
+    return DP == 256 ? 1 : DP == 128 ? (plain && bf16 ? 3 : 2) : 3;
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -148,12 +147,12 @@ __device__ __forceinline__ int steps_of(const Args &a, int len) { return (int)((
 // and three for fp32: with one part their rounding would be as large as the
 // output's own.  Sums and statistics are fp32.
 template <int DP, bool EXACT, bool I8, bool BF16, bool MASKED, bool TRACK, bool DIRECT>
-__global__ void __launch_bounds__(waves_of(DP, DIRECT) * 64) __attribute__((amdgpu_waves_per_eu(DIRECT ? 1 : resident(DP, EXACT && !MASKED, BF16, I8)))) attend_kernel(Args a) {
+__global__ void __launch_bounds__(waves_of(DP, DIRECT) * 64) __attribute__((amdgpu_waves_per_eu(DIRECT ? 1 : resident(DP, EXACT && !MASKED, BF16)))) attend_kernel(Args a) {
     constexpr int QP = BF16 ? 1 : 3, PP = BF16 ? 2 : 3;
     constexpr int KS = DP / 32;                  // products along d
     constexpr int W = DP == 64 ? 4 : 8;          // d of one value load
     constexpr int NU = DP / (16 * W);            // value loads of a token
-    constexpr int H = blocks_of(DP, I8, BF16), TILE = 16 * H, STEP = step_of(DP, I8, BF16, DIRECT);
+    constexpr int H = kBlocks, TILE = kTile, STEP = step_of(DP, DIRECT);
     constexpr int kWaves = waves_of(DP, DIRECT), kThreads = kWaves * 64;
     __shared__ float s_m[kWaves][16], s_l[kWaves][16];
     __shared__ float s_o[kWaves][16][DP + 4];
@@ -444,53 +443,49 @@ __global__ void __launch_bounds__(waves_of(DP, DIRECT) * 64) __attribute__((amdg
                     for (int u = 0; u < NU; ++u) vreg[i][u] = u4{0, 0, 0, 0};
                 }
         }
-        // two blocks are the 32 tokens of a product
+        u4 pp[PP];
 #pragma unroll
-        for (int y2 = 0; y2 < H / 2; ++y2) {
-            u4 pp[PP];
+        for (int i = 0; i < 4; ++i) {
+            uint32_t x[PP];
+            split2<PP>(p[2 * i], p[2 * i + 1], x);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t x[PP];
-                split2<PP>(p[8 * y2 + 2 * i], p[8 * y2 + 2 * i + 1], x);
+            for (int n = 0; n < PP; ++n) pp[n][i] = x[n];
+        }
 #pragma unroll
-                for (int n = 0; n < PP; ++n) pp[n][i] = x[n];
-            }
+        for (int u = 0; u < NU; ++u) {
+            if constexpr (!I8) {
 #pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                if constexpr (!I8) {
+                for (int j = 0; j < W; ++j) {
+                    u4 t;
 #pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        u4 t;
+                    for (int i = 0; i < 4; ++i)
+                        t[i] = __builtin_amdgcn_perm(vreg[2 * i + 1][u][j / 2], vreg[2 * i][u][j / 2], j & 1 ? 0x07060302u : 0x05040100u);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            t[i] = __builtin_amdgcn_perm(vreg[8 * y2 + 2 * i + 1][u][j / 2], vreg[8 * y2 + 2 * i][u][j / 2], j & 1 ? 0x07060302u : 0x05040100u);
+                    for (int n = 0; n < PP; ++n) o[u][j] = mfma(t, pp[n], o[u][j]);
+                }
+            } else {
+                // four d at a time: the 4 x 4 bytes of four tokens turned, then
+                // widened, are the operand's two dwords of those tokens
 #pragma unroll
-                        for (int n = 0; n < PP; ++n) o[u][j] = mfma(t, pp[n], o[u][j]);
+                for (int c = 0; c < W / 4; ++c) {
+                    uint32_t t[2][4];
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int at = 4 * hf;
+                        turn4(vreg[at][u][c], vreg[at + 1][u][c], vreg[at + 2][u][c], vreg[at + 3][u][c], t[hf]);
                     }
-                } else {
-                    // four d at a time: the 4 x 4 bytes of four tokens turned, then
-                    // widened, are the operand's two dwords of those tokens
 #pragma unroll
-                    for (int c = 0; c < W / 4; ++c) {
-                        uint32_t t[2][4];
+                    for (int j = 0; j < 4; ++j) {
+                        const u2 x = widen4(t[0][j]), y = widen4(t[1][j]);
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            const int at = 8 * y2 + 4 * hf;
-                            turn4(vreg[at][u][c], vreg[at + 1][u][c], vreg[at + 2][u][c], vreg[at + 3][u][c], t[hf]);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const u2 x = widen4(t[0][j]), y = widen4(t[1][j]);
-#pragma unroll
-                            for (int n = 0; n < PP; ++n) o[u][4 * c + j] = mfma(u4{x[0], x[1], y[0], y[1]}, pp[n], o[u][4 * c + j]);
-                        }
+                        for (int n = 0; n < PP; ++n) o[u][4 * c + j] = mfma(u4{x[0], x[1], y[0], y[1]}, pp[n], o[u][4 * c + j]);
                     }
                 }
             }
-            load_v(step + 1, 2 * y2, more);
-            load_v(step + 1, 2 * y2 + 1, more);
-            __builtin_amdgcn_sched_barrier(0);
         }
+#pragma unroll
+        for (int hf = 0; hf < H; ++hf) load_v(step + 1, hf, more);
+        __builtin_amdgcn_sched_barrier(0);
     }
 
     // join the waves: o of lane (head col, g4) is d = W (4 g4 + i) + 16 W u + j
@@ -769,11 +764,11 @@ Plan plan_of(const rq_kv_cache *c, int q_heads, int64_t max_len, int track) {
     const int64_t rows = (int64_t)c->batch * c->heads * p.tiles;
     // (tracked: where the workgroup has all of a key-value head's query heads)
     p.direct = (!track || p.tiles == 1) && rows <= (1 << 20) && (max_len <= kDirect || (rows >= device_cus() && max_len <= 4 * rows));
-    p.score_ld = (int)((max_len + 63) / 64 * 64);   // whole steps of a wave are written
+    p.score_ld = (int)((max_len + kTile - 1) / kTile * kTile);   // whole steps of a wave are written
     auto round = [](size_t n) { return (n + 15) / 16 * 16; };
     p.scores = track ? round((size_t)rows * p.tile_heads * p.score_ld * 4) : 0;
     if (p.direct) return p;
-    // (the least step, whatever the type of the queries: the workspace does not depend on it)
+    // (the least step, whatever the head size)
     const int64_t steps = rows * ((max_len + kLeastStep - 1) / kLeastStep);
     p.groups = (int)std::max<int64_t>(1, std::min<int64_t>({steps, (int64_t)device_cus() * kGroupsPerCu, kMaxGroups}));
     const size_t parts = (size_t)(p.groups + rows) * p.tile_heads;
@@ -797,7 +792,7 @@ int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_
     const Plan p = plan_of(c, q_heads, max_len, track);
     // as many shares as are resident at once
     const int DP = c->head_dim > 128 ? 256 : c->head_dim > 64 ? 128 : 64;
-    const int fit = device_cus() * std::min(kGroupsPerCu, resident(DP, c->head_dim == DP && !mask, bf16, c->dtype == RQ_I8));
+    const int fit = device_cus() * std::min(kGroupsPerCu, resident(DP, c->head_dim == DP && !mask, bf16));
     const unsigned groups = p.direct ? (unsigned)c->batch * c->heads * p.tiles : (unsigned)std::min(p.groups, fit);
     const int64_t heads = (int64_t)c->batch * q_heads;
     const int64_t weights = track ? (max_len + kJoin * 4 - 1) / (kJoin * 4) * c->batch * c->heads : 0;
@@ -817,7 +812,7 @@ int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_
     a.scores = reinterpret_cast<float *>(ws + p.part + p.stat + p.ends);
     a.q_ld = q_ld, a.out_ld = out_ld, a.mask_ld = mask_ld;
     a.hq = q_heads, a.G = q_heads / c->heads, a.tiles = p.tiles, a.tile_heads = p.tile_heads;
-    a.max_len = (int)max_len, a.score_ld = p.score_ld, a.step_log = ilog2(step_of(DP, c->dtype == RQ_I8, bf16, p.direct));
+    a.max_len = (int)max_len, a.score_ld = p.score_ld, a.step_log = ilog2(step_of(DP, p.direct));
     a.scale2 = scale * 1.4426950408889634f;
     hipStream_t s = static_cast<hipStream_t>(stream);
     auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(groups), dim3(waves_of(DP, p.direct) * 64), 0, s, a); };
