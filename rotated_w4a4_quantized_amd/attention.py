@@ -76,20 +76,32 @@ class DecodeAttention:
         self.workspace = torch.empty((max(n, 16),), dtype=torch.uint8, device=device)
 
     def step(self, x, stream=None):
-        """x [batch][hidden] bf16: the new tokens.  Returns y [batch][hidden]."""
+        """x [batch][hidden] bf16: the new tokens.  Returns y [batch][hidden],
+        which the next step overwrites.  Everything runs on `stream` (a torch
+        stream or its address; default: torch's current one)."""
+        if stream is None:
+            return self._step(x)
+        import torch
+        # (the block's own counters are torch operations, which go to the current stream)
+        device = self.y.device
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+        with torch.cuda.stream(stream):
+            return self._step(x)
+
+    def _step(self, x):
         if self.length >= self.room:
             raise ValueError(f"the cache holds {self.room} tokens a sequence")
         self.lens.add_(1)
         self.length += 1
-        self.qkv_proj(x, self.qkv, stream)
-        rq.qk_norm_rope(self.norm, self.qkv, self.q, positions=self.position, cache=self.cache, place=self.place,
-                        stream=stream)
+        self.qkv_proj(x, self.qkv)
+        rq.qk_norm_rope(self.norm, self.qkv, self.q, positions=self.position, cache=self.cache, place=self.place)
         rq.paged_attention(self.q, self.cache, self.lens, self.attn, max_len=self.length, track=self.track,
-                           workspace=self.workspace, stream=stream)
-        self.out_proj(self.attn, self.y, stream)
+                           workspace=self.workspace)
+        self.out_proj(self.attn, self.y)
         if self.track and self.length == self.room and self.room > self.budget:
             rq.cache_evict(self.cache, self.lens, self.budget, recent=min(self.recent, self.budget), sink=self.sink,
-                           max_len=self.length, workspace=self.workspace, stream=stream)
+                           max_len=self.length, workspace=self.workspace)
             self.length = self.budget
         self.place.copy_(self.lens)
         self.position.add_(1)

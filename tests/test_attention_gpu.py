@@ -684,3 +684,33 @@ def test_decode_command_runs(capsys):
     from rotated_w4a4_quantized_amd import attention
     attention.main(["--steps", "40", "--batch", "2", "--budget", "16"])
     assert "40 steps of 2 sequences" in capsys.readouterr().out
+
+
+def test_decode_block_steps_on_another_stream():
+    """Steps on a side stream give the bits of steps on the default one,
+    through evictions, while the default stream is kept busy."""
+    from rotated_w4a4_quantized_amd.attention import DecodeAttention
+    rng = np.random.default_rng(41)
+    hidden, hq, hkv, D, B, steps = 256, 8, 2, 64, 3, 60
+    Ws = [(rng.standard_normal(s) * 0.05).astype(np.float32) for s in (((hq + 2 * hkv) * D, hidden), (hidden, hq * D))]
+    x, _ = rand(rng, (steps, B, hidden), "bf16")
+    got = {}
+    for how in ("default", "stream", "address"):
+        blk = DecodeAttention(*Ws, hq, hkv, D, B, max_len=steps, budget=24, slack=8, recent=4, sink=2, page=16)
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        busy = torch.ones(2048, 2048, device="cuda")
+        ys = []
+        for t in range(steps):
+            if how == "default":
+                ys.append(blk.step(x[t]).clone())
+                continue
+            busy @ busy                                   # (work that a stray operation would queue behind)
+            y = blk.step(x[t], stream=s if how == "stream" else s.cuda_stream)
+            with torch.cuda.stream(s):
+                ys.append(y.clone())
+        torch.cuda.synchronize()
+        got[how] = ys + [blk.cache.k, blk.cache.v, blk.cache.weight, blk.cache.pos, blk.lens, blk.place, blk.position]
+    for how in ("stream", "address"):
+        for i, (a, b) in enumerate(zip(got["default"], got[how])):
+            assert same_bits(a, b), (how, i)

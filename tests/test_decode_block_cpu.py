@@ -1,0 +1,74 @@
+"""The decode block's own bookkeeping without a GPU: its buffers lie in host
+memory and the library's calls are replaced by records of them."""
+import contextlib
+
+import numpy as np
+import pytest
+
+from rotated_w4a4_quantized_amd import attention, rq
+
+torch = pytest.importorskip("torch")
+
+HIDDEN, HQ, HKV, D = 128, 4, 2, 32
+
+
+def block(calls, monkeypatch, **kw):
+    """A block whose library calls are appended to `calls` as (name, what
+    the call would read of the block's counters)."""
+    rng = np.random.default_rng(0)
+    weights = [rng.standard_normal(s).astype(np.float32) for s in (((HQ + 2 * HKV) * D, HIDDEN), (HIDDEN, HQ * D))]
+    args = dict(batch=2, max_len=40, page=16, device="cpu")
+    args.update(kw)
+    blk = attention.DecodeAttention(*weights, HQ, HKV, D, **args)
+
+    def record(name, *keys):
+        def f(*a, **k):
+            calls.append((name, {n: k[n].clone() if torch.is_tensor(k[n]) else k[n] for n in keys if n in k},
+                          blk.lens.clone(), k.get("stream")))
+        return f
+
+    monkeypatch.setattr(rq, "rotate_quant", record("rotate"))
+    monkeypatch.setattr(rq, "w4a4_linear", record("linear"))
+    monkeypatch.setattr(rq, "qk_norm_rope", record("norm", "positions", "place"))
+    monkeypatch.setattr(rq, "paged_attention", record("attend", "max_len"))
+
+    def evict(cache, lens, keep, **k):
+        calls.append(("evict", dict(keep=keep, **{n: k[n] for n in ("recent", "sink", "max_len")}), lens.clone(), k.get("stream")))
+        lens.clamp_(max=keep)
+    monkeypatch.setattr(rq, "cache_evict", evict)
+    return blk
+
+
+def x(n=2):
+    return torch.zeros(n, HIDDEN, dtype=torch.bfloat16)
+
+
+def test_step_on_a_stream_runs_all_of_it_there(monkeypatch):
+    """The library's calls and the block's own torch operations (which go to
+    the current stream) are on one stream, the one given."""
+    from torch.utils._python_dispatch import TorchDispatchMode
+    calls, current, ops = [], [], []
+    blk = block(calls, monkeypatch, budget=4, slack=2, recent=1, sink=0)
+
+    @contextlib.contextmanager
+    def use(s):
+        current.append(s)
+        yield
+        current.pop()
+
+    class Operations(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            if func.__name__.split(".")[0] in ("add_", "copy_"):
+                ops.append(list(current))
+            return func(*args, **(kwargs or {}))
+
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    s = object()
+    for _ in range(8):
+        before = len(calls), len(ops)
+        with Operations():
+            blk.step(x(), stream=s)
+        assert current == []
+        assert len(ops) >= before[1] + 3 and all(o == [s] for o in ops[before[1]:])
+        assert len(calls) >= before[0] + 6 and all(c[3] in (None, s) for c in calls[before[0]:])
+    assert any(c[0] == "evict" for c in calls)
