@@ -44,7 +44,8 @@ class DecodeAttention:
     """Attention of `batch` sequences that grow by one token a step.
 
     Wqkv [(q_heads + 2 kv_heads) * head_dim][hidden] and Wo [hidden][q_heads *
-    head_dim] fp32.  budget: tokens a sequence keeps (None: all of max_len);
+    head_dim] fp32.  max_len: tokens a sequence ever has, evicted ones included
+    (a step past it is refused).  budget: tokens a sequence keeps (None: all of max_len);
     the cache holds budget + slack, and is cut back to the budget when full,
     keeping the newest `recent` and the first `sink` tokens whatever their
     weight."""
@@ -70,6 +71,7 @@ class DecodeAttention:
         self.place, self.lens = new(1, i32)[:, 0], new(1, i32)[:, 0]
         self.position = new(1, i32)[:, 0]
         self.length = 0                     # tokens of a sequence in the cache (the same for all)
+        self.max_len, self.tokens = max_len, 0   # tokens that went through, evicted ones included
         n = rq.paged_attention_workspace_bytes(self.cache, q_heads, room, track=self.track)
         if self.track:
             n = max(n, rq.cache_evict_workspace_bytes(self.cache, budget, room))
@@ -90,6 +92,8 @@ class DecodeAttention:
             return self._step(x)
 
     def _step(self, x):
+        if self.tokens >= self.max_len:     # (eviction frees slots, but no rows of the rotation's table)
+            raise ValueError(f"the block was made for sequences of {self.max_len} tokens")
         if self.length >= self.room:
             raise ValueError(f"the cache holds {self.room} tokens a sequence")
         self.lens.add_(1)
@@ -105,6 +109,7 @@ class DecodeAttention:
             self.length = self.budget
         self.place.copy_(self.lens)
         self.position.add_(1)
+        self.tokens += 1
         return self.y
 
 

@@ -72,3 +72,21 @@ def test_step_on_a_stream_runs_all_of_it_there(monkeypatch):
         assert len(ops) >= before[1] + 3 and all(o == [s] for o in ops[before[1]:])
         assert len(calls) >= before[0] + 6 and all(c[3] in (None, s) for c in calls[before[0]:])
     assert any(c[0] == "evict" for c in calls)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(budget=8, slack=4, recent=2, sink=1), dict(budget=60)])
+def test_positions_stay_within_the_rotation_table(monkeypatch, kw):
+    """Steps up to max_len use rows 0 .. max_len - 1 of the table; the next is
+    refused and changes nothing, however often tokens were evicted."""
+    calls = []
+    blk = block(calls, monkeypatch, max_len=30, **kw)
+    for _ in range(30):
+        blk.step(x())
+    used = [c[1]["positions"].tolist() for c in calls if c[0] == "norm"]
+    assert used == [[i, i] for i in range(30)]
+    assert blk.norm.c.table_rows == 30
+    state = blk.length, blk.lens.tolist(), blk.place.tolist(), blk.position.tolist(), len(calls)
+    for _ in range(2):
+        with pytest.raises(ValueError):
+            blk.step(x())
+    assert state == (blk.length, blk.lens.tolist(), blk.place.tolist(), blk.position.tolist(), len(calls))
