@@ -48,11 +48,17 @@ class DecodeAttention:
     (a step past it is refused).  budget: tokens a sequence keeps (None: all of max_len);
     the cache holds budget + slack, and is cut back to the budget when full,
     keeping the newest `recent` and the first `sink` tokens whatever their
-    weight."""
+    weight.  Where the budget does not hold both, the first tokens take all of
+    it but one place, and the newest what is left."""
 
     def __init__(self, Wqkv, Wo, q_heads, kv_heads, head_dim, batch, max_len, budget=None, slack=64,
                  recent=32, sink=4, page=64, int8=False, rope_base=1e4, device="cuda"):
         import torch
+        # (protected tokens tie and ties go to the lower slot, so more of them
+        # than the budget would push out the newest)
+        if budget is not None:
+            sink = min(sink, budget - min(recent, 1))
+            recent = min(recent, budget - sink)
         self.batch, self.budget, self.recent, self.sink = batch, budget, recent, sink
         room = max_len if budget is None else min(max_len, budget + slack)
         bf16, i32 = torch.bfloat16, torch.int32
@@ -104,7 +110,7 @@ class DecodeAttention:
                            workspace=self.workspace)
         self.out_proj(self.attn, self.y)
         if self.track and self.length == self.room and self.room > self.budget:
-            rq.cache_evict(self.cache, self.lens, self.budget, recent=min(self.recent, self.budget), sink=self.sink,
+            rq.cache_evict(self.cache, self.lens, self.budget, recent=self.recent, sink=self.sink,
                            max_len=self.length, workspace=self.workspace)
             self.length = self.budget
         self.place.copy_(self.lens)

@@ -714,3 +714,29 @@ def test_decode_block_steps_on_another_stream():
     for how in ("stream", "address"):
         for i, (a, b) in enumerate(zip(got["default"], got[how])):
             assert same_bits(a, b), (how, i)
+
+
+def test_decode_block_with_a_budget_below_its_protected_tokens():
+    """Defaults that protect more than the budget: the first and the newest
+    tokens stay, the one just added among them."""
+    from rotated_w4a4_quantized_amd.attention import DecodeAttention
+    rng = np.random.default_rng(42)
+    hidden, hq, hkv, D, B, steps = 128, 4, 2, 32, 2, 100
+    Ws = [(rng.standard_normal(s) * 0.05).astype(np.float32) for s in (((hq + 2 * hkv) * D, hidden), (hidden, hq * D))]
+    blk = DecodeAttention(*Ws, hq, hkv, D, B, max_len=steps, budget=16, slack=20, page=16)   # recent 32, sink 4
+    evictions = 0
+    for t in range(steps):
+        n = blk.length + 1
+        blk.step(rand(rng, (B, hidden), "bf16")[0])
+        if blk.length == n:
+            continue
+        evictions += 1
+        pos = np.sort(blk.cache.pos.cpu().numpy()[:, :, :16], -1)
+        assert (pos == np.concatenate([np.arange(4), np.arange(t - 11, t + 1)])).all()
+    assert evictions == 1 + (steps - 36) // 20
+
+
+def test_decode_command_evicts(capsys):
+    from rotated_w4a4_quantized_amd import attention
+    attention.main(["--steps", "100", "--batch", "2", "--budget", "16"])
+    assert "100 steps of 2 sequences" in (text := capsys.readouterr().out) and "36 tokens of 100 kept" in text

@@ -90,3 +90,33 @@ def test_positions_stay_within_the_rotation_table(monkeypatch, kw):
         with pytest.raises(ValueError):
             blk.step(x())
     assert state == (blk.length, blk.lens.tolist(), blk.place.tolist(), blk.position.tolist(), len(calls))
+
+
+@pytest.mark.parametrize("budget,slack,recent,sink", [
+    (16, 64, 32, 4), (16, 8, 16, 4), (8, 4, 2, 8), (8, 4, 0, 20), (1, 3, 5, 5), (2, 1, 1, 1), (20, 6, 12, 8), (24, 8, 4, 2)])
+def test_the_newest_and_the_first_tokens_survive(monkeypatch, budget, slack, recent, sink):
+    """What the block asks of the eviction keeps both groups (the plain
+    eviction's result, random weights)."""
+    from tests import _attention as A
+    calls = []
+    steps = 90
+    blk = block(calls, monkeypatch, max_len=steps, budget=budget, slack=slack, recent=recent, sink=sink)
+    rng = np.random.default_rng(budget)
+    pos, weight, evictions = [], [], 0
+    first = min(sink, budget - min(recent, 1))
+    newest = min(recent, budget - first)
+    for t in range(steps):
+        before = len(calls)
+        blk.step(x())
+        pos, weight = pos + [t], weight + [float(rng.exponential())]
+        for name, k, _, _ in calls[before:]:
+            if name != "evict":
+                continue
+            evictions += 1
+            assert k["keep"] == budget and k["max_len"] == len(pos)
+            _, come = A.evict_row(np.array(weight, np.float32), np.array(pos), len(pos), k["keep"], k["recent"], k["sink"])
+            pos, weight = [pos[j] for j in come], [weight[j] for j in come]
+            assert len(pos) == budget
+            assert set(range(t - newest + 1, t + 1)) <= set(pos), "the newest stay"
+            assert set(range(first)) <= set(pos), "the first stay"
+    assert evictions >= 1
