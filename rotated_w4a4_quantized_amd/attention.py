@@ -26,7 +26,7 @@ class DecodeLinear:
     def __init__(self, W: np.ndarray, max_tokens: int, block=128, seed=0, device="cuda"):
         import torch
         rng = np.random.default_rng(seed)
-        N, K = W.shape
+        N, K = self.shape = W.shape
         rot = rq.Rotation.rpbh(rng.choice([-1, 1], K), rng.permutation(K), block)
         self.q, self.drot = rq.Quant.int4(), rot.to_device(device)
         self.dw = rq.pack_weights(rot, self.q, W).to_device(device)
@@ -35,7 +35,14 @@ class DecodeLinear:
         self.scale = torch.empty((max_tokens,), dtype=torch.float32, device=device)
 
     def __call__(self, X, Y, stream=None):
-        T = int(X.shape[0])
+        T, (N, K) = int(X.shape[0]), self.shape
+        if X.shape != (T, K) or T > self.scale.shape[0] or Y.shape != (T, N):
+            raise ValueError(f"expected at most {self.scale.shape[0]} rows of {K} values in and as many of {N} out, "
+                             f"got {tuple(X.shape)} and {tuple(Y.shape)}")
+        if not (X.is_contiguous() and Y.is_contiguous()):
+            raise ValueError("the rows must be contiguous")
+        if X.device != self.scale.device or Y.device != self.scale.device:
+            raise ValueError(f"the layer is on {self.scale.device}, its rows on {X.device} and {Y.device}")
         rq.rotate_quant(self.drot, self.q, X, self.codes[:T], self.scale[:T], stream=stream)
         rq.w4a4_linear(self.dw, self.codes[:T], self.scale[:T], Y, stream=stream)
 
@@ -54,6 +61,8 @@ class DecodeAttention:
     def __init__(self, Wqkv, Wo, q_heads, kv_heads, head_dim, batch, max_len, budget=None, slack=64,
                  recent=32, sink=4, page=64, int8=False, rope_base=1e4, device="cuda"):
         import torch
+        if Wqkv.shape[:1] != ((q_heads + 2 * kv_heads) * head_dim,) or Wo.shape[1:] != (q_heads * head_dim,):
+            raise ValueError(f"Wqkv {Wqkv.shape} and Wo {Wo.shape} are not of {q_heads} + 2 * {kv_heads} heads of {head_dim}")
         # (protected tokens tie and ties go to the lower slot, so more of them
         # than the budget would push out the newest)
         if budget is not None:
@@ -102,9 +111,11 @@ class DecodeAttention:
             raise ValueError(f"the block was made for sequences of {self.max_len} tokens")
         if self.length >= self.room:
             raise ValueError(f"the cache holds {self.room} tokens a sequence")
+        if x.shape[:1] != (self.batch,):
+            raise ValueError(f"expected a token of each of {self.batch} sequences, got {tuple(x.shape)}")
+        self.qkv_proj(x, self.qkv)          # (refuses a wrong x before anything has changed)
         self.lens.add_(1)
         self.length += 1
-        self.qkv_proj(x, self.qkv)
         rq.qk_norm_rope(self.norm, self.qkv, self.q, positions=self.position, cache=self.cache, place=self.place)
         rq.paged_attention(self.q, self.cache, self.lens, self.attn, max_len=self.length, track=self.track,
                            workspace=self.workspace)

@@ -120,3 +120,56 @@ def test_the_newest_and_the_first_tokens_survive(monkeypatch, budget, slack, rec
             assert set(range(t - newest + 1, t + 1)) <= set(pos), "the newest stay"
             assert set(range(first)) <= set(pos), "the first stay"
     assert evictions >= 1
+
+
+@pytest.mark.parametrize("bad", [
+    lambda: x(3), lambda: x(1), lambda: x(0), lambda: torch.zeros(2, HIDDEN + 128, dtype=torch.bfloat16),
+    lambda: torch.zeros(2, HIDDEN - 1, dtype=torch.bfloat16), lambda: torch.zeros(2 * HIDDEN, dtype=torch.bfloat16),
+    lambda: torch.zeros(2, 1, HIDDEN, dtype=torch.bfloat16),
+    lambda: x().to("meta"), lambda: torch.zeros(HIDDEN, 2, dtype=torch.bfloat16).t(),
+    lambda: torch.zeros(2, 2 * HIDDEN, dtype=torch.bfloat16)[:, :HIDDEN]])
+def test_step_refuses_tokens_that_do_not_fit_its_buffers(monkeypatch, bad):
+    """Before any call of the library, which takes addresses and row counts
+    as they are, and before any counter moves."""
+    calls = []
+    blk = block(calls, monkeypatch)
+    blk.step(x())
+    blk.step(x().float())
+    state = blk.length, blk.tokens, blk.lens.tolist(), blk.place.tolist(), blk.position.tolist(), len(calls)
+    with pytest.raises(ValueError):
+        blk.step(bad())
+    assert state == (blk.length, blk.tokens, blk.lens.tolist(), blk.place.tolist(), blk.position.tolist(), len(calls))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float64])
+def test_step_refuses_types_before_counters_move(dtype):
+    rng = np.random.default_rng(0)
+    blk = attention.DecodeAttention(*[rng.standard_normal(s).astype(np.float32) for s in (((HQ + 2 * HKV) * D, HIDDEN), (HIDDEN, HQ * D))],
+                                    HQ, HKV, D, 2, 40, page=16, device="cpu")
+    with pytest.raises(KeyError):
+        blk.step(x().to(dtype))
+    assert (blk.length, blk.tokens, blk.lens.tolist(), blk.place.tolist(), blk.position.tolist()) == (0, 0, [0, 0], [0, 0], [0, 0])
+
+
+def test_weights_of_another_shape_are_refused(monkeypatch):
+    good = np.zeros(((HQ + 2 * HKV) * D, HIDDEN), np.float32), np.zeros((HIDDEN, HQ * D), np.float32)
+    for Wqkv, Wo in ((np.zeros(((HQ + 2 * HKV) * D + 8, HIDDEN), np.float32), good[1]),
+                     (good[0], np.zeros((HIDDEN, HQ * D + 128), np.float32)), (good[0][:-1], good[1])):
+        with pytest.raises(ValueError):
+            attention.DecodeAttention(Wqkv, Wo, HQ, HKV, D, 2, 40, page=16, device="cpu")
+
+
+def test_linear_refuses_rows_that_do_not_fit(monkeypatch):
+    calls = []
+    monkeypatch.setattr(rq, "rotate_quant", lambda *a, **k: calls.append(a))
+    monkeypatch.setattr(rq, "w4a4_linear", lambda *a, **k: calls.append(a))
+    layer = attention.DecodeLinear(np.zeros((24, 128), np.float32), 4, device="cpu")
+    X, Y = torch.zeros(4, 128), torch.zeros(4, 24)
+    layer(X, Y)
+    layer(X[:2], Y[:2].bfloat16())
+    assert len(calls) == 4
+    for a, b in ((torch.zeros(5, 128), torch.zeros(5, 24)), (X, Y[:3]), (X, torch.zeros(4, 25)), (X[:, :64], Y),
+                 (X, torch.zeros(24, 4).t()), (X, Y.to("meta"))):
+        with pytest.raises(ValueError):
+            layer(a, b)
+    assert len(calls) == 4
