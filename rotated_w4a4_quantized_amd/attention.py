@@ -53,7 +53,8 @@ class DecodeAttention:
     Wqkv [(q_heads + 2 kv_heads) * head_dim][hidden] and Wo [hidden][q_heads *
     head_dim] fp32.  max_len: tokens a sequence ever has, evicted ones included
     (a step past it is refused).  budget: tokens a sequence keeps (None: all of max_len);
-    the cache holds budget + slack, and is cut back to the budget when full,
+    the cache holds budget + slack (one more than the budget at least), and is
+    cut back to the budget when full,
     keeping the newest `recent` and the first `sink` tokens whatever their
     weight.  Where the budget does not hold both, the first tokens take all of
     it but one place, and the newest what is left."""
@@ -69,7 +70,7 @@ class DecodeAttention:
             sink = min(sink, budget - min(recent, 1))
             recent = min(recent, budget - sink)
         self.batch, self.budget, self.recent, self.sink = batch, budget, recent, sink
-        room = max_len if budget is None else min(max_len, budget + slack)
+        room = max_len if budget is None else min(max_len, budget + max(slack, 1))
         bf16, i32 = torch.bfloat16, torch.int32
         self.qkv_proj = DecodeLinear(Wqkv, batch, seed=1, device=device)
         self.out_proj = DecodeLinear(Wo, batch, seed=2, device=device)

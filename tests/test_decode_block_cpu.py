@@ -173,3 +173,12 @@ def test_linear_refuses_rows_that_do_not_fit(monkeypatch):
         with pytest.raises(ValueError):
             layer(a, b)
     assert len(calls) == 4
+
+
+def test_a_budget_without_slack_evicts_every_step(monkeypatch):
+    calls = []
+    blk = block(calls, monkeypatch, budget=5, slack=0, recent=2, sink=1)
+    for t in range(20):
+        blk.step(x())
+        assert blk.length == min(t + 1, 5) and blk.lens.tolist() == [blk.length] * 2
+    assert sum(c[0] == "evict" for c in calls) == 15
