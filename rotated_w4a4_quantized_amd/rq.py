@@ -640,6 +640,10 @@ class QKNorm:
             if cos is None or sin is None or cos.dim() != 2 or cos.shape != sin.shape:
                 raise ValueError("cos and sin must be [rows][rot_dim / 2] tensors of one shape")
             rows, half = cos.shape
+        held = [t for t in (cos, sin, q_weight, k_weight) if t is not None]
+        for t in held[1:]:
+            if t.device != held[0].device:
+                raise ValueError(f"the weights and tables are on {held[0].device} and {t.device}")
         self.c = c_qk_norm(q_heads, kv_heads, head_dim, 2 * half, int(bool(interleaved)), rows,
                            eps, 0, _vector(q_weight, head_dim, torch.float32, "q_weight"),
                            _vector(k_weight, head_dim, torch.float32, "k_weight"),

@@ -247,3 +247,13 @@ def test_int8_rule_by_hand():
     codes, s = A.int8_rule(np.array([[0, 0, 0], [-2, 1.25, 0.005], [127, 1, -0.5]], np.float32))
     assert codes.tolist() == [[0, 0, 0], [-127, 79, 0], [127, 1, 0]]
     assert s[0] == 0 and s[2] == 1
+
+
+@pytest.mark.parametrize("apart", ["cos", "sin", "q_weight", "k_weight"])
+def test_head_norm_of_tables_on_several_devices_is_refused(apart):
+    """The kernel takes addresses; one of host memory among the GPU's would be read there."""
+    parts = dict(cos=torch.zeros(8, 32), sin=torch.zeros(8, 32), q_weight=torch.ones(64), k_weight=torch.ones(64))
+    rq.QKNorm(4, 2, 64, **parts)
+    parts[apart] = parts[apart].to("meta")
+    with pytest.raises(ValueError):
+        rq.QKNorm(4, 2, 64, **parts)

@@ -740,3 +740,11 @@ def test_decode_command_evicts(capsys):
     from rotated_w4a4_quantized_amd import attention
     attention.main(["--steps", "100", "--batch", "2", "--budget", "16"])
     assert "100 steps of 2 sequences" in (text := capsys.readouterr().out) and "36 tokens of 100 kept" in text
+
+
+@pytest.mark.parametrize("host", ["tables", "weights"])
+def test_qk_norm_rope_refuses_tables_in_host_memory(host):
+    tables = dict(cos=torch.zeros(8, 32), sin=torch.zeros(8, 32)) if host == "tables" else dict(q_weight=torch.ones(64), k_weight=torch.ones(64))
+    x = torch.zeros(2, 512, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        rq.qk_norm_rope(rq.QKNorm(4, 2, 64, **tables), x, torch.zeros_like(x[:, :256]), k_out=torch.zeros_like(x[:, :128]))
