@@ -558,6 +558,16 @@ def _vector(t, n, dtype, name):
     return t.data_ptr()
 
 
+def _workspace(t):
+    """Address and bytes of a workspace (None: none).  A view that repeats or
+    skips elements has other memory than its element count says."""
+    if t is None:
+        return None, 0
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _on_device(index, *tensors):
     """Refuse buffers that are not all on the current GPU (index: the first
     one's get_device(), -1 for host memory)."""
@@ -712,13 +722,13 @@ def paged_attention(q, cache: KVCache, lens, out, scale=None, max_len=None, mask
         if cache.weight is None:
             raise ValueError("track needs a cache with weight")
         weight_out = cache.weight if weight_out is None else weight_out
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    p_ws, ws_bytes = _workspace(workspace)
     _check(load().rq_paged_attention(
         cache._ref, p_q, dt, q_ld, width // D, D ** -0.5 if scale is None else scale,
         _vector(lens, B, torch.int32, "lens"), max_len, p_m, m_ld, p_o, o_ld,
         _vector(lse, B * (width // D), torch.float32, "lse"), int(track),
         _vector(weight_out, B * cache.heads * cache.slots, torch.float32, "weight_out") if track else None,
-        None if workspace is None else workspace.data_ptr(), ws_bytes, _stream(stream)))
+        p_ws, ws_bytes, _stream(stream)))
 
 
 def cache_evict_workspace_bytes(cache: KVCache, keep: int, max_len: int) -> int:
@@ -739,10 +749,10 @@ def cache_evict(cache: KVCache, lens, keep, recent=0, sink=0, max_len=None, lens
     _on_device(cache.k.get_device(), lens, lens_out, weight_out, pos_out, workspace)
     n = B * cache.heads * cache.slots
     p_lens = _vector(lens, B, torch.int32, "lens")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    p_ws, ws_bytes = _workspace(workspace)
     _check(load().rq_cache_evict(
         cache._ref, p_lens, cache.slots if max_len is None else max_len, keep, recent, sink,
         p_lens if lens_out is None else _vector(lens_out, B, torch.int32, "lens_out"),
         cache.c.weight if weight_out is None else _vector(weight_out, n, torch.float32, "weight_out"),
         cache.c.pos if pos_out is None else _vector(pos_out, n, torch.int32, "pos_out"),
-        None if workspace is None else workspace.data_ptr(), ws_bytes, _stream(stream)))
+        p_ws, ws_bytes, _stream(stream)))

@@ -257,3 +257,12 @@ def test_head_norm_of_tables_on_several_devices_is_refused(apart):
     parts[apart] = parts[apart].to("meta")
     with pytest.raises(ValueError):
         rq.QKNorm(4, 2, 64, **parts)
+
+
+def test_workspace_of_the_binding():
+    """A repeated element claims bytes that are not there."""
+    ws = torch.zeros(64, dtype=torch.uint8)
+    assert rq._workspace(None) == (None, 0) and rq._workspace(ws) == (ws.data_ptr(), 64)
+    for bad in (ws[:1].expand(1 << 20), ws[::2], ws.reshape(8, 8).t()):
+        with pytest.raises(ValueError):
+            rq._workspace(bad)

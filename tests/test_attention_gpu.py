@@ -748,3 +748,18 @@ def test_qk_norm_rope_refuses_tables_in_host_memory(host):
     x = torch.zeros(2, 512, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(ValueError):
         rq.qk_norm_rope(rq.QKNorm(4, 2, 64, **tables), x, torch.zeros_like(x[:, :256]), k_out=torch.zeros_like(x[:, :128]))
+
+
+def test_workspaces_that_repeat_or_skip_memory_are_refused():
+    rng = np.random.default_rng(43)
+    cache, *_ = build(rng, 1, 1, 64, 16, [4000], "bf16", True)
+    cache = rq.KVCache(cache.k, cache.v, cache.table, weight=cache.weight, pos=torch.zeros_like(cache.weight, dtype=torch.int32))
+    q = torch.zeros(1, 64, dtype=torch.bfloat16, device="cuda")
+    tl = torch.tensor([4000], dtype=torch.int32, device="cuda")
+    n = max(rq.paged_attention_workspace_bytes(cache, 1, 4000, True), rq.cache_evict_workspace_bytes(cache, 100, 4000))
+    one = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    for ws in (one[:1].expand(n), torch.zeros(2 * n, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            rq.paged_attention(q, cache, tl, torch.empty_like(q), max_len=4000, track=True, workspace=ws)
+        with pytest.raises(ValueError):
+            rq.cache_evict(cache, tl, 100, max_len=4000, workspace=ws)
