@@ -663,14 +663,16 @@ typedef struct rq_qk_norm {
  * rounded once, to the output's type or to the cache's.  Cache, RQ_I8: the
  * symmetric 8-bit rule of rq_rotate_quant over the head's fp32 values: s =
  * fl32(amax / 127), code = rne(fl32(y * fl32(127 / amax))); amax == 0 gives
- * codes 0, s = 0.
+ * codes 0, s = 0.  A head with a NaN or an infinity gets codes 0 and a scale of
+ * NaN or infinity, so all of it reads back as NaN.
  * Arguments:
  *   d          host descriptor
  *   qkv        device [T][ld], dtype RQ_F32 or RQ_BF16
  *   ld         elements from row to row, >= the row above
  *   T          tokens, 0 <= T < 2^31
  *   positions  device int32 [T] rows of cos and sin, NULL: row t.  A position
- *              outside [0, table_rows) gives NaN in the rotated coordinates.
+ *              outside [0, table_rows) gives NaN in the rotated coordinates
+ *              (RQ_I8 cache: in the whole stored key).
  *   q_out      device, row t at t * q_ld: q_heads * D values of dtype.  May be
  *              qkv itself with q_ld == ld (in place).
  *   k_out      device, row t at t * k_ld: kv_heads * D values of dtype, or

@@ -98,8 +98,10 @@ __device__ __forceinline__ uint32_t codes4(const float *x, float inv) {
     uint32_t r = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        // (|x inv| <= 127 but for rounding and NaN)
-        const int c = (int)fminf(fmaxf(rintf(x[i] * inv), -127.0f), 127.0f);
+        // (|x inv| <= 127 but for rounding; NaN, from a value or from 0 times an
+        // infinity, gives 0)
+        const float y = x[i] * inv;
+        const int c = y == y ? (int)fminf(fmaxf(rintf(y), -127.0f), 127.0f) : 0;
         r |= (uint32_t)(c & 0xff) << (8 * i);
     }
     return r;
@@ -215,11 +217,14 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(Args a) {
                 const int64_t row = row0 + (int64_t)kh * page;
                 void *store = is_v ? a.c.v : a.c.k;
                 if (I8) {
-                    float amax = 0.0f;
+                    // the largest magnitude by its bits: they are ordered, with NaN above
+                    // all, which the scale then carries (a float maximum would drop it)
+                    uint32_t top = 0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(y[i]));
+                    for (int i = 0; i < 8; ++i) top = max(top, __builtin_bit_cast(uint32_t, y[i]) & 0x7fffffffu);
 #pragma unroll
-                    for (int o = 1; o < LP; o *= 2) amax = fmaxf(amax, __shfl_xor(amax, o));
+                    for (int o = 1; o < LP; o *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+                    const float amax = __builtin_bit_cast(float, top);
                     const float inv = amax > 0.0f ? 127.0f / amax : 0.0f;
                     if (kept && live) {
                         char *o = static_cast<char *>(store) + row * D;

@@ -763,3 +763,51 @@ def test_workspaces_that_repeat_or_skip_memory_are_refused():
             rq.paged_attention(q, cache, tl, torch.empty_like(q), max_len=4000, track=True, workspace=ws)
         with pytest.raises(ValueError):
             rq.cache_evict(cache, tl, 100, max_len=4000, workspace=ws)
+
+
+@pytest.mark.parametrize("D,rot,inter", [(64, 64, False), (128, 128, True), (80, 40, False)])
+def test_int8_cache_keeps_what_is_not_finite(D, rot, inter):
+    """Heads with NaN or infinities read back as NaN from an int8 cache, others
+    as without them, and attention over such a sequence is NaN, not a number."""
+    rng = np.random.default_rng(D)
+    T, hq, hkv, page, rows = 12, 4, 2, 16, 50
+    x = (rng.standard_normal((T, hq + 2 * hkv, D)) * 2).astype(np.float32)
+    clean = x.copy()
+    v = x[:, hq + hkv:]
+    x[1, hq, 3] = np.nan
+    x[2, hq + 1, D - 1] = np.inf
+    v[3, 0, 0], v[4, 1, 5], v[5, 0, 7] = np.nan, np.inf, -np.inf
+    v[6, 0, :], v[6, 0, 4] = 0, 1e-38                    # 127 / amax overflows: zeros stay zeros
+    positions = rng.integers(0, rows, T).astype(np.int32)
+    outside = positions.copy()
+    outside[7], outside[8] = -1, rows
+    ang = rng.uniform(-4, 4, (rows, rot // 2))
+    dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    nrm = rq.QKNorm(hq, hkv, D, cos=dev(np.cos(ang).astype(np.float32)), sin=dev(np.sin(ang).astype(np.float32)), interleaved=inter)
+    place = torch.zeros(T, dtype=torch.int32, device="cuda")
+    got = []
+    for data, pos in ((clean, positions), (x, outside)):
+        c = rq.KVCache.alloc(T, hkv, D, page, page=page, int8=True)
+        q = torch.empty(T, hq * D, device="cuda")
+        rq.qk_norm_rope(nrm, dev(data).reshape(T, -1), q, positions=dev(pos), cache=c, place=place)
+        got.append((c, q))
+    bad = {"k": [(1, 0), (2, 1), (7, 0), (7, 1), (8, 0), (8, 1)], "v": [(3, 0), (4, 1), (5, 0)]}
+    (c0, q0), (c1, q1) = got
+    for n in "kv":
+        codes, scale = getattr(c1, n)[:, :, 0].cpu().numpy(), getattr(c1, n + "_scale")[:, :, 0].cpu().numpy()
+        with np.errstate(invalid="ignore"):
+            back = codes * scale[..., None]
+        for t in range(T):
+            for h in range(hkv):
+                if (t, h) in bad[n]:
+                    assert np.isnan(back[t, h]).all() and (codes[t, h] == 0).all(), (n, t, h)
+                elif (n, t, h) != ("v", 6, 0):
+                    assert np.array_equal(codes[t, h], getattr(c0, n)[t, h, 0].cpu().numpy()), (n, t, h)
+                    assert scale[t, h] == getattr(c0, n + "_scale")[t, h, 0].item()
+    assert c1.v[6, 0, 0].tolist() == [127 if d == 4 else 0 for d in range(D)]
+    out, lse = run_attend(c1, q0, torch.ones(T, dtype=torch.int32, device="cuda"), 1)
+    nan = torch.isnan(out.reshape(T, hkv, hq // hkv, D)).all(-1).all(-1).cpu().numpy()
+    finite = torch.isfinite(out.reshape(T, hkv, hq // hkv, D)).all(-1).all(-1).cpu().numpy()
+    for t in range(T):
+        for h in range(hkv):
+            assert (nan if (t, h) in bad["k"] + bad["v"] else finite)[t, h], (t, h)
