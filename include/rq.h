@@ -713,6 +713,8 @@ rq_status rq_paged_attention_workspace_bytes(const rq_kv_cache *cache, int32_t q
  *   w_j = exp(s_j - lse);  out[d] = sum_j w_j v_j[d]
  * Where no slot is left (length 0, all masked): out is 0 and lse -infinity.
  * Keys and values of slots that are left out may hold anything, NaN included.
+ * A NaN among a head's scores makes its out, its lse and the weights of all its
+ * slots that are not left out NaN.
  * Arguments:
  *   cache      the cache; batch is the number of queries
  *   q          device, row b at b * q_ld: q_heads * D values of dtype (RQ_F32

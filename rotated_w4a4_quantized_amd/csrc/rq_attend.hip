@@ -121,6 +121,25 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[PARTS]) {
 __device__ __forceinline__ int length_of(const Args &a, int b) { return min(max(a.lens[b], 0), a.max_len); }
 __device__ __forceinline__ int steps_of(const Args &a, int len) { return (int)((uint32_t)(len + (1 << a.step_log) - 1) >> a.step_log); }
 
+// In a row whose sum is NaN every weight is, save those of slots that are left
+// out: their scores are -infinity for all heads, and they receive nothing.
+template <class Scores>
+__device__ __forceinline__ void clear_left_out(f4 &add, int heads, Scores scores) {
+    const float x[4] = {add[0], add[1], add[2], add[3]};
+    if (x[0] == x[0] && x[1] == x[1] && x[2] == x[2] && x[3] == x[3]) return;
+    float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // (NaN counts as a score)
+    for (int g = 0; g < heads; ++g) {
+        const f4 s = scores(g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float y = s[e];
+            most[e] = y == -INFINITY ? most[e] : 0.0f;
+        }
+    }
+    add = f4{x[0] == x[0] || most[0] == 0.0f ? x[0] : 0.0f, x[1] == x[1] || most[1] == 0.0f ? x[1] : 0.0f,
+             x[2] == x[2] || most[2] == 0.0f ? x[2] : 0.0f, x[3] == x[3] || most[3] == 0.0f ? x[3] : 0.0f};
+}
+
 // A row is one (sequence, key-value head, tile of up to 16 query heads).
 //
 // DIRECT: one workgroup takes one row and writes its output.  Otherwise the
@@ -491,6 +510,9 @@ __global__ void __launch_bounds__(waves_of(DP, DIRECT) * 64) __attribute__((amdg
     // join the waves: o of lane (head col, g4) is d = W (4 g4 + i) + 16 W u + j
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
+    // A NaN score is in l, but maxima drop it.  A maximum of infinity takes it
+    // through every join: exp2(inf - inf) is NaN, other parts count 0 beside it.
+    if (l != l) m = INFINITY;
     if (g4 == 0) {
         s_m[wave][col] = m;
         s_l[wave][col] = l;
@@ -563,6 +585,7 @@ __global__ void __launch_bounds__(waves_of(DP, DIRECT) * 64) __attribute__((amdg
 #pragma unroll
                 for (int e = 0; e < 4; ++e) add[e] += __builtin_amdgcn_exp2f(x[e] - s_fin[0][g]) * s_fin[1][g];
             }
+            clear_left_out(add, heads, [&](int g) { return *reinterpret_cast<const f4 *>(sc + g * 16); });
             for (int e = 0; e < 4; ++e)
                 if (j + e < len) a.weight_out[at + e] = before[e] + add[e];
         }
@@ -734,6 +757,7 @@ __global__ void __launch_bounds__(kJoin) join_kernel(Args a, int outs) {
                 take(scores(g0 + g), g);
         }
     }
+    if (j < len) clear_left_out(add, a.G, scores);
     w += add;
     if (j + 4 <= len) *reinterpret_cast<f4 *>(a.weight_out + at) = w;
     else

@@ -811,3 +811,64 @@ def test_int8_cache_keeps_what_is_not_finite(D, rot, inter):
     for t in range(T):
         for h in range(hkv):
             assert (nan if (t, h) in bad["k"] + bad["v"] else finite)[t, h], (t, h)
+
+
+NANS = [
+    # B, hq, hkv, D, page, lengths, type, cache: one workgroup a row, then shares, then many shares a row
+    (3, 8, 2, 64, 16, [300, 17, 211], "bf16", "bf16"),
+    (3, 8, 2, 128, 32, [300, 64, 500], "f32", "int8"),
+    (3, 6, 1, 256, 16, [300, 65, 40], "bf16", "bf16"),
+    (2, 8, 2, 64, 16, [3000, 900], "f32", "bf16"),
+    (2, 4, 2, 128, 64, [9000, 4000], "bf16", "int8"),
+    (2, 48, 2, 64, 16, [700, 2100], "bf16", "bf16"),
+    (130, 4, 2, 64, 16, [1500 if i == 1 else 200 + 7 * i for i in range(130)], "bf16", "bf16"),
+]
+
+
+@pytest.mark.parametrize("B,hq,hkv,D,page,lens,dtype,kind", NANS)
+@pytest.mark.parametrize("track", [False, True])
+def test_paged_attention_nan_scores_show_everywhere(B, hq, hkv, D, page, lens, dtype, kind, track):
+    """A NaN query, or a NaN key that is not masked: out, lse and weights of its
+    heads are NaN, however tokens are dealt out to waves and workgroups; masked
+    slots receive nothing and other rows are as ever."""
+    rng = np.random.default_rng(B + D + hq)
+    cache, k, v, table, weight = build(rng, B, hkv, D, page, lens, kind, track)
+    q, qx = rand(rng, (B, hq * D), dtype, 2.0)
+    n = max(lens)
+    G = hq // hkv
+    mask = (rng.random((B, n)) < 0.7).astype(np.uint8)
+    mask[0, 5], mask[:, 0] = 1, 1
+    h1 = hkv - 1
+    q[1, h1 * G * D + 3] = np.nan                       # the first query head of the last key-value head
+    at = int(table[0, 5 // page]), 0, 5 % page          # token 5 of key-value head 0 of sequence 0
+    if kind == "int8":
+        cache.k_scale[at] = np.nan
+    else:
+        cache.k[at][D // 2] = np.nan
+    out, lse = run_attend(cache, q, torch.tensor(lens, dtype=torch.int32, device="cuda"), n, torch.from_numpy(mask).cuda(), track)
+    o, ls = num(out).reshape(B, hkv, G, D), num(lse).reshape(B, hkv, G)
+    bad = np.zeros((B, hkv, G), bool)
+    bad[0, 0, :], bad[1, h1, 0] = True, True
+    assert np.isnan(o[bad]).all() and np.isnan(ls[bad]).all()
+    assert np.isfinite(o[~bad]).all() and np.isfinite(ls[~bad]).all()
+    wo = num(cache.weight) if track else None
+    for b, h in [(0, 0), (0, h1), (1, 0), (1, h1), (B - 1, h1)]:
+        j = np.arange(lens[b])
+        keep = mask[b, :lens[b]] != 0
+        pg = table[b, j // page]
+        want, wl, w, ds, mag = A.attention(qx.reshape(B, hkv, G, D)[b, h].astype(np.float64), k[pg, h, j % page], v[pg, h, j % page], keep, D ** -0.5)
+        rel = 2 * ds[:, None] + 64 * U
+        bound = A.unit(dtype) * np.abs(want) + rel * mag + 1e-37 + (2.0 ** -16 * mag if dtype == "bf16" else 0)
+        ok = ~bad[b, h]
+        assert (np.abs(o[b, h] - want) <= bound)[ok].all()
+        assert (np.abs(ls[b, h] - wl) <= ds + 16 * U * (np.abs(wl) + 1))[ok].all()
+        if not track:
+            continue
+        left_out = np.ones(wo.shape[2], bool)
+        left_out[j[keep]] = False
+        assert np.array_equal(wo[b, h][left_out], weight[b, h][left_out].astype(np.float64)), "slots left out receive nothing"
+        if bad[b, h].any():
+            assert np.isnan(wo[b, h][~left_out]).all()
+        else:
+            sums = weight[b, h, j] + w.sum(0)
+            assert (np.abs(wo[b, h, j] - sums) <= (w * rel).sum(0) + 4 * U * np.abs(sums))[keep].all()
