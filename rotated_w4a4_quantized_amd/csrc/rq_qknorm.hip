@@ -107,6 +107,14 @@ __device__ __forceinline__ uint32_t codes4(const float *x, float inv) {
     return r;
 }
 
+// 1 / sqrt(x).  The instruction takes numbers below 2^-126 for 0, which a small
+// eps lets through; scaling by powers of two is exact.
+__device__ __forceinline__ float inv_root(float x) {
+    const bool tiny = x < 0x1p-100f;
+    const float r = __builtin_amdgcn_rsqf(tiny ? x * 0x1p64f : x);
+    return tiny ? r * 0x1p32f : r;
+}
+
 // A head is LP lanes (a power of two, 8 D's values each); a wave holds 64 / LP
 // heads of one token at a time and walks over the token's heads, with the
 // token's cosines and sines and both weights in registers.  LP divides a wave,
@@ -187,7 +195,7 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(Args a) {
                     for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
                     for (int o = 1; o < LP; o *= 2) ss += __shfl_xor(ss, o);
-                    const float r = __builtin_amdgcn_rsqf(fmaf(ss, inv_d, a.eps));
+                    const float r = inv_root(fmaf(ss, inv_d, a.eps));
 #pragma unroll
                     for (int i = 0; i < 8; ++i) y[i] = x[i] * r * (is_q ? wq[i] : wk[i]);
                     if (turned) {

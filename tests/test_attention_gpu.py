@@ -872,3 +872,25 @@ def test_paged_attention_nan_scores_show_everywhere(B, hq, hkv, D, page, lens, d
         else:
             sums = weight[b, h, j] + w.sum(0)
             assert (np.abs(wo[b, h, j] - sums) <= (w * rel).sum(0) + 4 * U * np.abs(sums))[keep].all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_qk_norm_rope_of_tiny_heads(dtype):
+    """Mean squares below 2^-126 (eps 0, or as small) give heads of mean square
+    1 like any others.  Bound: each square and each sum of the mean is off by half
+    the least fp32 step, 2^-150, in sum over D values and the division by D by less
+    than 2^-148 absolutely, so a root by half of 2^-148 / mean relatively."""
+    rng = np.random.default_rng(44)
+    D, scales = 64, [1e-17, 3e-19, 1e-19, 5e-20, 2e-20, 1e-20]
+    q, x = rand(rng, (len(scales), D), "f32")
+    x = (x * np.array(scales, np.float32)[:, None]).astype(np.float32)
+    if dtype == "bf16":
+        x = A.bf16(x)
+    q = torch.from_numpy(x).cuda().to(TYPES[dtype])
+    for eps in (0.0, 1e-40):
+        out = torch.empty_like(q)
+        rq.qk_norm_rope(rq.QKNorm(1, 0, D, eps=eps), q, out)
+        ms = (x.astype(np.float64) ** 2).mean(-1, keepdims=True) + float(np.float32(eps))
+        want = x / np.sqrt(ms)
+        rel = A.unit(dtype) + 40 * U + 2.0 ** -148 / ms
+        assert (np.abs(num(out) - want) <= rel * np.abs(want)).all(), np.abs(num(out) / want - 1).max(-1)
