@@ -731,7 +731,9 @@ rq_status rq_paged_attention_workspace_bytes(const rq_kv_cache *cache, int32_t q
  *   lse        device fp32 [batch][q_heads] or NULL
  *   track      1: add up the weights: weight_out[b][h][j] = weight[b][h][j] +
  *              sum of w_j over h's query heads, for j < min(lens[b], max_len)
- *              (slots past that are not written)
+ *              (slots past that are not written).  A launch holds such a call
+ *              as long as batch * (heads * ceil(max_len / 1024) + ceil(q_heads
+ *              / 4)) < 2^24 - 1024; larger ones may be refused (RQ_ERR_SHAPE).
  *   weight_out device fp32, shaped as the cache's weight and possibly the same
  *              buffer; used with track only
  *   workspace  device scratch of rq_paged_attention_workspace_bytes(), 16-byte
@@ -768,7 +770,9 @@ rq_status rq_cache_evict_workspace_bytes(const rq_kv_cache *cache, int32_t keep,
  *              in place.  A slot without a page moves weight and pos only.
  *   lens       device int32 [batch]
  *   max_len    host bound of lens, 0 <= max_len <= table_ld * page
- *   keep       tokens that stay, >= 1
+ *   keep       tokens that stay, >= 1.  What a launch holds: batch * heads <
+ *              2^22 and batch * heads * ceil(min(keep, max_len - keep) / 64) +
+ *              ceil(batch / 256) < 2^24; beyond: RQ_ERR_SHAPE.
  *   recent, sink  >= 0; positions are >= 0
  *   lens_out   device int32 [batch]: min(n, keep); may be lens
  *   weight_out, pos_out  shaped as the cache's weight and pos and possibly the

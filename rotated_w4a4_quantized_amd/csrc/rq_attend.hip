@@ -777,7 +777,9 @@ constexpr int kDirect = 512;
 constexpr int kGroupsPerCu = 3;
 struct Plan {
     bool direct;
+    bool many;                         // join: a wave a head instead of a workgroup
     int tiles, tile_heads, groups, score_ld;
+    int64_t outs, weights;             // join: workgroups for outputs and for weights
     size_t part, stat, ends, scores;   // bytes
 };
 Plan plan_of(const rq_kv_cache *c, int q_heads, int64_t max_len, int track) {
@@ -799,10 +801,20 @@ Plan plan_of(const rq_kv_cache *c, int q_heads, int64_t max_len, int track) {
     p.part = round(parts * c->head_dim * 4);
     p.stat = round(parts * 8);
     p.ends = round((size_t)rows * 8);
+    // a wave a head once that fills the device
+    const int64_t heads = (int64_t)c->batch * q_heads;
+    p.many = heads >= 4 * device_cus();
+    p.outs = p.many ? (heads + kJoin / 64 - 1) / (kJoin / 64) : heads;
+    p.weights = track ? (max_len + kJoin * 4 - 1) / (kJoin * 4) * c->batch * c->heads : 0;
     return p;
 }
 
 }  // namespace
+
+bool attend_fits(const rq_kv_cache *c, int q_heads, int64_t max_len, int track) {
+    const Plan p = plan_of(c, q_heads, max_len, track);
+    return p.outs + p.weights < (1 << 24);   // (of kJoin threads: a launch holds 2^32)
+}
 
 size_t attend_workspace_bytes(const rq_kv_cache *c, int q_heads, int64_t max_len, int track) {
     const Plan p = plan_of(c, q_heads, max_len, track);
@@ -818,13 +830,6 @@ int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_
     const int DP = c->head_dim > 128 ? 256 : c->head_dim > 64 ? 128 : 64;
     const int fit = device_cus() * std::min(kGroupsPerCu, resident(DP, c->head_dim == DP && !mask, bf16));
     const unsigned groups = p.direct ? (unsigned)c->batch * c->heads * p.tiles : (unsigned)std::min(p.groups, fit);
-    const int64_t heads = (int64_t)c->batch * q_heads;
-    const int64_t weights = track ? (max_len + kJoin * 4 - 1) / (kJoin * 4) * c->batch * c->heads : 0;
-    // a wave a head once that fills the device
-    const bool many = heads >= 4 * device_cus();
-    const int64_t outs = many ? (heads + kJoin / 64 - 1) / (kJoin / 64) : heads;
-    // (workgroups of 256: a launch holds 2^24 of them)
-    if (!p.direct && outs + weights >= (1 << 24)) return (int)hipErrorInvalidValue;
     Args a{};
     a.c = device_cache(c);
     a.q = q, a.out = out, a.lens = lens, a.mask = mask, a.lse = lse;
@@ -868,9 +873,9 @@ int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_
     else if (c->head_dim <= 128) dims(std::integral_constant<int, 128>{});
     else dims(std::integral_constant<int, 256>{});
     if (!p.direct) {
-        auto join = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((unsigned)(outs + weights)), dim3(kJoin), 0, s, a, (int)outs); };
-        if (bf16) many ? join(join_kernel<true, 64>) : join(join_kernel<true, kJoin>);
-        else many ? join(join_kernel<false, 64>) : join(join_kernel<false, kJoin>);
+        auto join = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((unsigned)(p.outs + p.weights)), dim3(kJoin), 0, s, a, (int)p.outs); };
+        if (bf16) p.many ? join(join_kernel<true, 64>) : join(join_kernel<true, kJoin>);
+        else p.many ? join(join_kernel<false, 64>) : join(join_kernel<false, kJoin>);
     }
     return (int)hipGetLastError();
 }

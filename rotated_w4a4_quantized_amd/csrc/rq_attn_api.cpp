@@ -1,6 +1,7 @@
 // rq_attn_api.cpp -- entry points of the attention around the linears: head
 // norm with rotation and cache store, paged single-token attention, eviction.
-// Argument validation and dispatch; every check runs before any HIP call.
+// Argument validation and dispatch.  Every check runs before the first launch;
+// sizes of workspaces and grids follow the device's number of CUs (read once).
 
 #include <hip/hip_runtime.h>
 
@@ -62,14 +63,20 @@ rq_status check_attention(const rq_kv_cache *c, int q_heads, int64_t max_len, in
     if (q_heads < 1 || q_heads > 1024 || q_heads % c->heads != 0)
         return fail(RQ_ERR_SHAPE, "q_heads must be a multiple of the cache's heads, at most 1024");
     if (track != 0 && track != 1) return fail(RQ_ERR_SHAPE, "track must be 0 or 1");
-    return check_max_len(c, max_len);
+    if ((st = check_max_len(c, max_len)) != RQ_OK) return st;
+    if (!attend_fits(c, q_heads, max_len, track))
+        return fail(RQ_ERR_SHAPE, "batch, heads and max_len of a tracked call need more workgroups than a launch holds");
+    return RQ_OK;
 }
 
 rq_status check_evict(const rq_kv_cache *c, int keep, int64_t max_len, bool buffers) {
     rq_status st = check_cache(c, buffers);
     if (st != RQ_OK) return st;
     if (keep < 1) return fail(RQ_ERR_SHAPE, "keep must be at least 1");
-    return check_max_len(c, max_len);
+    if ((st = check_max_len(c, max_len)) != RQ_OK) return st;
+    if (!evict_fits(c, keep, max_len))
+        return fail(RQ_ERR_SHAPE, "batch, heads and moves need more workgroups than a launch holds");
+    return RQ_OK;
 }
 
 }  // namespace

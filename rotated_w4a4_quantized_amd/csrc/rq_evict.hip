@@ -405,7 +405,17 @@ int most_moves(int keep, int64_t max_len) {
     return (int)std::max<int64_t>(0, std::min<int64_t>(keep, max_len - keep));
 }
 
+// workgroups of move_kernel: for a row's moves, and for the lengths
+int64_t move_chunks(int keep, int64_t max_len) { return (most_moves(keep, max_len) + kChunk - 1) / kChunk; }
+int64_t lens_groups_of(const rq_kv_cache *c) { return (c->batch + 255) / 256; }
+
 }  // namespace
+
+// (a launch holds 2^32 threads: 1024 a row for the selection, 256 a workgroup of the moves)
+bool evict_fits(const rq_kv_cache *c, int keep, int64_t max_len) {
+    const int64_t rows = (int64_t)c->batch * c->heads;
+    return rows < (1 << 22) && move_chunks(keep, max_len) * rows + lens_groups_of(c) < (1 << 24);
+}
 
 size_t evict_workspace_bytes(const rq_kv_cache *c, int keep, int64_t max_len) {
     const size_t rows = (size_t)c->batch * c->heads;
@@ -429,9 +439,7 @@ int launch_cache_evict(const rq_kv_cache *c, const int32_t *lens, int64_t max_le
     // Few moves are done by the workgroup that found them.  (Not with lens_out in
     // place: another row of the sequence may still have to read its length.)
     const bool fused = a.most <= kFused && lens_out != lens;
-    const int64_t chunks = (a.most + kChunk - 1) / kChunk, lens_groups = (c->batch + 255) / 256;
-    // (a launch holds 2^32 threads)
-    if (rows > (1 << 22) - 1 || chunks * rows + lens_groups > (1 << 24) - 1) return (int)hipErrorInvalidValue;
+    const int64_t chunks = move_chunks(keep, max_len), lens_groups = lens_groups_of(c);
     auto select = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(rows), dim3(kThreads), 0, s, a); };
     auto pick = [&](auto f) {
         constexpr bool F = decltype(f)::value;

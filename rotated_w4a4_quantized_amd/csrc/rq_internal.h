@@ -110,11 +110,14 @@ int launch_qk_norm_rope(const rq_qk_norm *d, const void *qkv, int bf16, int64_t 
                         const int32_t *positions, void *q_out, int64_t q_ld, void *k_out,
                         int64_t k_ld, const rq_kv_cache *cache, const int32_t *seq,
                         const int32_t *place, void *stream);
+// (the ..._fits: whether a call's workgroups fit a launch)
+bool attend_fits(const rq_kv_cache *c, int q_heads, int64_t max_len, int track);
 size_t attend_workspace_bytes(const rq_kv_cache *c, int q_heads, int64_t max_len, int track);
 int launch_paged_attention(const rq_kv_cache *c, const void *q, int bf16, int64_t q_ld, int q_heads,
                            float scale, const int32_t *lens, int64_t max_len, const uint8_t *mask,
                            int64_t mask_ld, void *out, int64_t out_ld, float *lse, int track,
                            float *weight_out, void *workspace, void *stream);
+bool evict_fits(const rq_kv_cache *c, int keep, int64_t max_len);
 size_t evict_workspace_bytes(const rq_kv_cache *c, int keep, int64_t max_len);
 int launch_cache_evict(const rq_kv_cache *c, const int32_t *lens, int64_t max_len, int keep,
                        int recent, int sink, int32_t *lens_out, float *weight_out,

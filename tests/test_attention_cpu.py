@@ -266,3 +266,31 @@ def test_workspace_of_the_binding():
     for bad in (ws[:1].expand(1 << 20), ws[::2], ws.reshape(8, 8).t()):
         with pytest.raises(ValueError):
             rq._workspace(bad)
+
+
+@pytest.mark.parametrize("batch,heads,q_heads,max_len,track,status", [
+    (65535, 1024, 1024, 64, 0, 0), (65535, 16, 16, 2048, 0, 0), (4096, 64, 64, 65536, 0, 0),
+    (65535, 1024, 1024, 1024, 1, SHAPE), (4096, 64, 64, 65536, 1, 0),   # (one workgroup a row: nothing to join)
+    (8192, 32, 1024, 65536, 1, SHAPE), (16384, 1024, 1024, 513, 1, SHAPE),
+    (16384, 512, 512, 513, 1, 0)])
+def test_attention_grids_that_no_launch_holds(batch, heads, q_heads, max_len, track, status):
+    """Refused by their sizes, also when the workspace is asked for, before anything is launched."""
+    n = ctypes.c_size_t(0)
+    c = cache(batch=batch, heads=heads, table_ld=4096)
+    assert rq.load().rq_paged_attention_workspace_bytes(ctypes.byref(c), q_heads, max_len, track, ctypes.byref(n)) == status
+    if status:
+        row = q_heads * 64
+        assert call_attend(c, heads=q_heads, max_len=max_len, track=track, weight_out=PTR, q_ld=row, out_ld=row, wsb=1 << 62) == status
+        assert b"launch" in rq.load().rq_last_error()
+
+
+@pytest.mark.parametrize("batch,heads,keep,max_len,status", [
+    (4096, 1023, 1, 2, 0), (4096, 1024, 1, 2, SHAPE), (65535, 1024, 100, 100, SHAPE), (65535, 64, 256, 1000, SHAPE),
+    (65535, 32, 448, 1000, 0), (65535, 32, 512, 1000, SHAPE), (16384, 1, 65536, 65536, 0), (1024, 64, 30000, 65536, SHAPE)])
+def test_eviction_grids_that_no_launch_holds(batch, heads, keep, max_len, status):
+    n = ctypes.c_size_t(0)
+    c = cache(batch=batch, heads=heads, table_ld=4096)
+    assert rq.load().rq_cache_evict_workspace_bytes(ctypes.byref(c), keep, max_len, ctypes.byref(n)) == status
+    if status:
+        assert call_evict(c, keep=keep, max_len=max_len, wsb=1 << 62) == status
+        assert b"launch" in rq.load().rq_last_error()
