@@ -545,8 +545,8 @@ def _rows(t, n, width, name):
         raise ValueError(f"{name} must be rows of {width} contiguous elements")
     if shape[0] != n:
         raise ValueError(f"{name} must have {n} rows, got {shape[0]}")
-    # (a single row has no stride to keep to)
-    return t.data_ptr(), stride[0] if n > 1 else have
+    # (a single row has no stride to keep to, nor an end beyond its width)
+    return t.data_ptr(), stride[0] if n > 1 else width
 
 
 def _vector(t, n, dtype, name):

@@ -294,3 +294,14 @@ def test_eviction_grids_that_no_launch_holds(batch, heads, keep, max_len, status
     if status:
         assert call_evict(c, keep=keep, max_len=max_len, wsb=1 << 62) == status
         assert b"launch" in rq.load().rq_last_error()
+
+
+def test_a_single_row_may_be_followed_by_any_number_of_elements():
+    """The row stride of one row is never used, so its multiple does not matter."""
+    row = torch.zeros(1, 67)
+    assert rq._rows(row, 1, 64, "q") == (row.data_ptr(), 64)
+    two = torch.zeros(2, 67)
+    assert rq._rows(two, 2, 64, "q") == (two.data_ptr(), 67)
+    assert rq._rows(two[:0], 0, 64, "q")[1] == 64
+    with pytest.raises(ValueError):
+        rq._rows(torch.zeros(1, 63), 1, 64, "q")

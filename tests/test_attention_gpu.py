@@ -894,3 +894,17 @@ def test_qk_norm_rope_of_tiny_heads(dtype):
         want = x / np.sqrt(ms)
         rel = A.unit(dtype) + 40 * U + 2.0 ** -148 / ms
         assert (np.abs(num(out) - want) <= rel * np.abs(want)).all(), np.abs(num(out) / want - 1).max(-1)
+
+
+def test_one_row_with_an_odd_number_of_elements_behind_it():
+    rng = np.random.default_rng(45)
+    hq, hkv, D = 4, 2, 64
+    n = (hq + 2 * hkv) * D
+    wide, x = rand(rng, (1, n + 3), "bf16")
+    ref, got = torch.empty(1, hq * D, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, hq * D + 5, dtype=torch.bfloat16, device="cuda")
+    cache, *_ = build(rng, 1, hkv, D, 16, [40], "bf16", False)
+    place = torch.tensor([39], dtype=torch.int32, device="cuda")
+    rq.qk_norm_rope(rq.QKNorm(hq, hkv, D), wide[:, :n].clone(), ref, cache=cache, place=place)
+    k = cache.k.clone()
+    rq.qk_norm_rope(rq.QKNorm(hq, hkv, D), wide, got, cache=cache, place=place)
+    assert same_bits(got[:, :hq * D], ref) and (got[:, hq * D:] == 0).all() and same_bits(cache.k, k)
