@@ -1,4 +1,4 @@
-// rq_attn_util.h -- device helpers shared by the attention kernels.
+// rq_attn_util.h -- the paged cache as the attention kernels take it.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -10,21 +10,6 @@
 
 namespace rq {
 namespace attn {
-
-__device__ __forceinline__ float bf16_f32(uint16_t b) { return __builtin_bit_cast(float, (uint32_t)b << 16); }
-// round to nearest even
-__device__ __forceinline__ uint16_t f32_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
-
-template <bool BF16>
-__device__ __forceinline__ float load1(const void *p, int64_t i) {
-    if constexpr (BF16) return bf16_f32(static_cast<const uint16_t *>(p)[i]);
-    else return static_cast<const float *>(p)[i];
-}
-template <bool BF16>
-__device__ __forceinline__ void store1(void *p, int64_t i, float v) {
-    if constexpr (BF16) static_cast<uint16_t *>(p)[i] = f32_bf16(v);
-    else static_cast<float *>(p)[i] = v;
-}
 
 // A cache as the kernels take it: slot j of (sequence b, head h) is row
 // (page * heads + h) * 2^page_log + j % 2^page_log of k and v.
