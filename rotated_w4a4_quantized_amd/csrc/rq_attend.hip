@@ -4,7 +4,7 @@
 //
 // The cache is read once and nothing else is large, so HBM bounds it: 131071
 // tokens of 8 heads x 128 in bf16 (537 MB) take 95 us, 5.7 TB/s, where a plain
-// read of as much takes 87 us; 262143 tokens in int8 108 us with the joining, 5.1
+// read of as much takes 87 us; 262143 tokens in int8 110 us with the joining, 5.0
 // TB/s.  The matrix cores are 5% busy; they are there because 4 to 16 query heads a key
 // would keep the vector units too busy to issue the loads.
 //
@@ -55,7 +55,8 @@ struct Args {
 constexpr int waves_of(int DP, bool direct) { return direct && DP <= 128 ? 8 : 4; }
 // 16-token blocks of one wave's step: the 32 tokens of one value product.  (4 for
 // int8, as many bytes as bf16, need the registers of a third wave: 48 uneven
-// sequences of up to 8190 tokens took 102 us against 86, 200 of 1000 78 against 60.)
+// sequences of up to 8190 tokens took 100 us against 93, 200 of 1000 111 against 95,
+// 96 of 8192 289 against 284; one of 262143 tokens 107 against 110.)
 constexpr int kBlocks = 2, kTile = 16 * kBlocks;
 // tokens of one workgroup's step
 constexpr int step_of(int DP, bool direct) { return waves_of(DP, direct) * kTile; }
@@ -647,7 +648,7 @@ __device__ __forceinline__ void join_stats(const f2 *st, int n, int stride, int 
 
 constexpr int kJoin = 256;     // threads of a joining workgroup
 
-// Joins the parts of rows (5 to 7 us; with the weights of 64 sequences of 4000
+// Joins the parts of rows (4 to 7 us; with the weights of 64 sequences of 4000
 // tokens 18 us, 50 MB).  The first outs workgroups write outputs, a head by
 // TPH threads each (all of a workgroup where heads are few, a wave where there
 // are many); the others add the weights of kJoin * 4 slots of one key-value
@@ -766,14 +767,17 @@ __global__ void __launch_bounds__(kJoin) join_kernel(Args a, int outs) {
 }
 
 // How a call is run.  Direct up to kDirect tokens: a workgroup walks them in
-// fewer microseconds than the joining kernel costs (8 sequences of 512 tokens: 9.4
-// us against 14.3).  Direct too where the rows fill the device and are many for
-// their length, so that uneven ones even out: 256 sequences of 2000 tokens, 8 heads
-// 350 us (6.0 TB/s) against 376, uneven 195 against 217; 128 of 4000, uneven 204
-// against 203; but 64 of up to 8000, uneven 221 against 197.
+// fewer microseconds than the joining kernel costs (8 sequences of 300 tokens: 8.3
+// us against 11.2; of 512 10.0 against 11.6; of 1024 14.6 against 15.2).  Direct too
+// where the rows fill the device and are many for their length, so that uneven ones
+// even out: 256 sequences of 2000 tokens, 8 heads 349 us (6.0 TB/s) against 371,
+// uneven 188 against 215; 128 of 4000, uneven 201 against 204; but 64 of up to 8000,
+// uneven 222 against 203.
 constexpr int kDirect = 512;
 // Shares per CU otherwise, at most: what is resident of the variant with the
-// fewest registers.
+// fewest registers.  With 3, 2, 1 of them 48 uneven int8 sequences take 96, 96, 107
+// us, 64 uneven tracked ones 257, 258, 262; a sequence alone would like fewer (131071
+// bf16 tokens 103, 98, 98, 262143 int8 ones 111, 108, 105).
 constexpr int kGroupsPerCu = 3;
 struct Plan {
     bool direct;
@@ -801,7 +805,9 @@ Plan plan_of(const rq_kv_cache *c, int q_heads, int64_t max_len, int track) {
     p.part = round(parts * c->head_dim * 4);
     p.stat = round(parts * 8);
     p.ends = round((size_t)rows * 8);
-    // a wave a head once that fills the device
+    // A wave a head once that fills the device: 4096 heads of 6000 tokens 528 us
+    // against 534 by a workgroup a head, 2048 of 4000 189 against 192, from 1280 down
+    // to 256 alike; 32 heads of 131071 tokens 113 against 103.
     const int64_t heads = (int64_t)c->batch * q_heads;
     p.many = heads >= 4 * device_cus();
     p.outs = p.many ? (heads + kJoin / 64 - 1) / (kJoin / 64) : heads;

@@ -7,7 +7,7 @@
 // Everything is read and written once: HBM bounds long calls (32760 tokens of 24
 // heads x 128 in bf16, 419 MB: 83 us, 5.06 TB/s, what a copy reaches), launch and
 // three dependent loads (place, page, and positions before cosines) the short ones
-// (one token of 40 heads: 4.1 us).
+// (one token of 40 heads: 4.0 us).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -274,14 +274,14 @@ int launch_qk_norm_rope(const rq_qk_norm *d, const void *qkv, int bf16, int64_t 
     const bool i8 = stored && cache->dtype == RQ_I8;
     const int lp = a.D <= 16 ? 2 : a.D <= 32 ? 4 : a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32;
     // A token's heads are dealt out to as many waves as make one round of what is
-    // resident (16 a CU): 1999 fp32 tokens of 24 small heads take 8.2 us, 10.2 in a
-    // round and a half; 2000 tokens of 24 x 128 in bf16 8.6 against 11.4.
+    // resident (16 a CU): 1999 fp32 tokens of 24 small heads take 8.7 us, and 10.5
+    // with a wave a group of heads; 2000 tokens of 24 x 128 in bf16 8.9 against 11.4.
     const int groups = (a.nh + 64 / lp - 1) / (64 / lp);
     const int64_t full = (int64_t)device_cus() * 16;
     a.per = (int)std::min<int64_t>(groups, std::max<int64_t>(1, (T * groups + full - 1) / full));
     a.chunks = (groups + a.per - 1) / a.per;
-    // Twice what is resident, then waves walk over visits: for 32760 tokens of 24
-    // heads that took 87 us (83 now), one visit a wave 101, a single round of waves 91.
+    // Twice what is resident, then waves walk over visits: 32760 tokens of 24 heads
+    // take 83 us, with a single round of waves 85, with one visit a wave 80.
     const int64_t wgs = std::min<int64_t>((T * a.chunks + 3) / 4, (int64_t)device_cus() * 8);
     auto go = [&](auto kern) {
         hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(256), 0, static_cast<hipStream_t>(stream), a);
