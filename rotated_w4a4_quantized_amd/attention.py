@@ -51,13 +51,13 @@ class DecodeAttention:
     """Attention of `batch` sequences that grow by one token a step.
 
     Wqkv [(q_heads + 2 kv_heads) * head_dim][hidden] and Wo [hidden][q_heads *
-    head_dim] fp32.  max_len: tokens a sequence ever has, evicted ones included
-    (a step past it is refused).  budget: tokens a sequence keeps (None: all of max_len);
-    the cache holds budget + slack (one more than the budget at least), and is
-    cut back to the budget when full,
-    keeping the newest `recent` and the first `sink` tokens whatever their
-    weight.  Where the budget does not hold both, the first tokens take all of
-    it but one place, and the newest what is left."""
+    head_dim] fp32.  max_len: tokens a sequence ever has, evicted ones
+    included (a step past it is refused).  budget: tokens a sequence keeps
+    (None: all of max_len); the cache holds budget + slack (one more than the
+    budget at least), and is cut back to the budget when full, keeping the
+    newest `recent` and the first `sink` tokens whatever their weight.  Where
+    the budget does not hold both, the first tokens take all of it but one
+    place, and the newest what is left."""
 
     def __init__(self, Wqkv, Wo, q_heads, kv_heads, head_dim, batch, max_len, budget=None, slack=64,
                  recent=32, sink=4, page=64, int8=False, rope_base=1e4, device="cuda"):
