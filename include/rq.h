@@ -2,7 +2,8 @@
  * rq.h -- C ABI of librq, the MI355X (gfx950) rotated low-bit quantized
  * linear layer of diffusion-transformer inference, and the attention between
  * such layers (head norm with rotation, paged cache, single-token attention,
- * eviction: the last part of this file).
+ * eviction; the residual stream with its norms, attention of many queries to
+ * the same keys: the last two parts of this file).
  *
  * The layer (pages: "TR-DQ: Time-Rotation Diffusion Quantization",
  * section 3.1 and Eq.(8)-(9); "OrbitQuant" abstract; "DiRotQ" abstract):
@@ -786,6 +787,182 @@ rq_status rq_cache_evict(const rq_kv_cache *cache, const int32_t *lens, int64_t 
                          int32_t keep, int32_t recent, int32_t sink, int32_t *lens_out,
                          float *weight_out, int32_t *pos_out, void *workspace,
                          size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Between the blocks, and attention of many queries to the same keys: the
+ * residual stream with the norms around it (rq_block_norm), attention to
+ * states of another length (rq_cross_attention), and attention of a batch
+ * whose sequences share the first part of their cache (rq_prefix_attention).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * A norm over rows of `width` values (host descriptor, device pointers).
+ *   RQ_NORM_RMS    x / sqrt(mean(x^2) + eps) * weight + bias
+ *   RQ_NORM_LAYER  the same of x - mean(x)
+ *   eps      finite, >= 0
+ *   weight, bias  device fp32 [width], 16-byte aligned, or NULL (ones, zeros)
+ */
+typedef enum rq_norm_kind { RQ_NORM_RMS = 0, RQ_NORM_LAYER = 1 } rq_norm_kind;
+typedef struct rq_norm {
+    int32_t kind;
+    float eps;
+    const float *weight;
+    const float *bias;
+} rq_norm;
+
+/*
+ * What a conditioning network gives a block (host descriptor, device
+ * pointers): rows of fp32 gates, shifts and scales.
+ *   rows    rows of the tables, 1 .. 2^31 - 1
+ *   ld      elements from row to row, >= width, ld % 4 == 0 (any with one row)
+ *   per     tokens of a row when index is NULL: token t takes row t / per (>= 1)
+ *   index   device int32 [T], the row of every token, or NULL.  A row outside
+ *           [0, rows) gives NaN in what the given tables reach.
+ *   gate, shift, scale  device fp32 [rows][ld], 16-byte aligned; each may be NULL
+ */
+typedef struct rq_modulation {
+    int32_t rows;
+    int32_t reserved;
+    int64_t ld;
+    int64_t per;
+    const int32_t *index;
+    const float *gate;
+    const float *shift;
+    const float *scale;
+} rq_modulation;
+
+/*
+ * The residual stream between two blocks, in one pass: the output y of the
+ * block before, normalized (post) and gated, is added to the stream x, and the
+ * sum is normalized (pre) and modulated for the block behind.  For each token,
+ * fp32 throughout:
+ *   h = alpha x + beta gate (.) post(y);   z = pre(h) (.) (1 + scale) + shift
+ * h and z are rounded once each (z is computed from h before its rounding).
+ * Arguments:
+ *   post, pre  norms, each may be NULL (none).  post needs y, pre needs z.
+ *   mod        modulations or NULL (gate 1, shift 0, scale 0)
+ *   width      K, 8 <= K <= 16384, K % 8 == 0
+ *   x          device, row t at t * x_ld: K values of x_dtype (RQ_F32 or RQ_BF16)
+ *   y          device, row t at t * y_ld: K values of dtype (RQ_F32 or RQ_BF16),
+ *              or NULL: h = alpha x
+ *   T          tokens, 0 <= T < 2^31
+ *   alpha, beta  finite
+ *   h          device, rows of x_dtype, or NULL; may be x with h_ld == x_ld
+ *   z          device, rows of dtype, or NULL; may be y with z_ld == y_ld.  h or z
+ *              must be given.  Rows must not overlap otherwise.
+ *   Rows of x, y, h, z must start 16-byte aligned.
+ * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_DTYPE, RQ_ERR_ALIGN, RQ_ERR_HIP.
+ */
+rq_status rq_block_norm(const rq_norm *post, const rq_norm *pre, const rq_modulation *mod,
+                        int32_t width, const void *x, int32_t x_dtype, int64_t x_ld, const void *y,
+                        int32_t dtype, int64_t y_ld, int64_t T, float alpha, float beta, void *h,
+                        int64_t h_ld, void *z, int64_t z_ld, void *stream);
+
+/*
+ * Keys and values of a batch, as a projection writes them (host descriptor,
+ * device pointers): token j of sequence b and head h is the head_dim values at
+ * b * stride + j * ld + h * head_dim.
+ *   heads     key-value heads, 1 .. 1024
+ *   head_dim  D, 16 <= D <= 256, D % 8 == 0
+ *   batch     sequences, 0 .. 65535
+ *   keys      tokens of a sequence, 0 .. 2^24
+ *   k_ld, v_ld          elements from token to token, >= heads * D, multiples of 8
+ *   k_stride, v_stride  elements from sequence to sequence, >= 0 (0: one for
+ *             all), multiples of 8
+ *   k, v      device bf16, 16-byte aligned
+ *   lens      device int32 [batch], tokens of each sequence (values are taken
+ *             into [0, keys]), or NULL: keys each
+ *   mask      device uint8 [batch], row b at b * mask_ld, or NULL: tokens with 0
+ *             are left out; mask_ld >= keys (or 0: one row for all)
+ */
+typedef struct rq_states {
+    int32_t heads;
+    int32_t head_dim;
+    int32_t batch;
+    int32_t reserved;
+    int64_t keys;
+    int64_t k_ld;
+    int64_t v_ld;
+    int64_t k_stride;
+    int64_t v_stride;
+    int64_t mask_ld;
+    const void *k;
+    const void *v;
+    const int32_t *lens;
+    const uint8_t *mask;
+} rq_states;
+
+/*
+ * Bytes of device workspace rq_cross_attention takes for these arguments.  It
+ * depends on the descriptor's sizes, the other arguments and the device.
+ * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_DTYPE.
+ */
+rq_status rq_cross_attention_workspace_bytes(const rq_states *states, int64_t queries, int32_t q_heads,
+                                             int32_t dtype, size_t *bytes);
+
+/*
+ * Attention of every query token to its sequence's states (an encoder's, or the
+ * block's own tokens; no causal order).  For sequence b, token t and query head
+ * i (of key-value head h = i / (q_heads / heads)), over the tokens j < lens[b]
+ * whose mask is not 0:
+ *   s_j = scale * sum_d q[d] k_j[d];  lse = log sum_j exp(s_j)
+ *   out[d] = sum_j exp(s_j - lse) v_j[d]
+ * Where no token is left: out is 0 and lse -infinity.  Keys and values that are
+ * left out may hold anything, NaN included.  A NaN among the scores of a row
+ * makes its out and lse NaN.
+ * Arguments:
+ *   states     keys and values; their batch is that of the queries
+ *   q          device, token t of sequence b at b * q_stride + t * q_ld: q_heads *
+ *              D values of dtype (RQ_F32 or RQ_BF16)
+ *   queries    tokens of a sequence, 0 .. 2^24; batch * queries * q_heads < 2^25
+ *   q_heads    a multiple of the states' heads, at most 1024
+ *   scale      multiplies the scores (finite)
+ *   q_lens     device int32 [batch] or NULL: tokens from q_lens[b] on are not
+ *              computed and their rows of out and lse not written
+ *   out        device, as q; must not alias q
+ *   lse        device fp32 [batch][queries][q_heads] or NULL
+ *   workspace  device scratch of rq_cross_attention_workspace_bytes(), 16-byte
+ *              aligned
+ *   Rows of q and out must start 16-byte aligned.
+ * Sums and softmax statistics are fp32.  The same inputs give the same bits.
+ * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_DTYPE, RQ_ERR_ALIGN, RQ_ERR_HIP.
+ */
+rq_status rq_cross_attention(const rq_states *states, const void *q, int32_t dtype, int64_t q_ld,
+                             int64_t q_stride, int64_t queries, int32_t q_heads, float scale,
+                             const int32_t *q_lens, void *out, int64_t out_ld, int64_t out_stride,
+                             float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Bytes of device workspace rq_prefix_attention takes for these arguments.  It
+ * depends on the cache's sizes, the other arguments and the device.
+ * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_DTYPE.
+ */
+rq_status rq_prefix_attention_workspace_bytes(const rq_kv_cache *cache, int32_t q_heads, int32_t dtype,
+                                              int64_t prefix, int64_t max_len, size_t *bytes);
+
+/*
+ * rq_paged_attention for a batch whose sequences share their first `prefix`
+ * tokens (a system prompt): these are read and computed once for all.  Slots j <
+ * prefix lie in the pages of prefix_table, the others in those of the cache's
+ * table as ever (its entries of pages that lie wholly below prefix are not
+ * read; a page that prefix ends in has the sequence's own copy).  The result is
+ * rq_paged_attention's with prefix_table's pages in front of every row of the
+ * table.  A sequence with lens[b] < prefix or lens[b] < 1 has no token in the
+ * batch: its out is 0 and its lse -infinity.
+ * Arguments as rq_paged_attention, and
+ *   prefix_table  device int32 [ceil(prefix / page)], 16-byte aligned (NULL when
+ *              prefix is 0).  An entry outside [0, pages): no page there.
+ *   prefix     0 <= prefix <= max_len
+ *   lens       device int32 [batch] tokens of a sequence, the prefix included
+ *   mask       columns below prefix are not read: all sequences see all of it
+ *   batch * q_heads < 2^25.
+ * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_DTYPE, RQ_ERR_ALIGN, RQ_ERR_HIP.
+ */
+rq_status rq_prefix_attention(const rq_kv_cache *cache, const int32_t *prefix_table, int64_t prefix,
+                              const void *q, int32_t dtype, int64_t q_ld, int32_t q_heads, float scale,
+                              const int32_t *lens, int64_t max_len, const uint8_t *mask, int64_t mask_ld,
+                              void *out, int64_t out_ld, float *lse, void *workspace,
+                              size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "librq.so")
 SOURCES = ["rq_host.cpp", "rq_api.cpp", "rq_device.cpp", "rq_rpbh.hip", "rq_dense.hip",
            "rq_gemm_w4a4.hip", "rq_gemm_i8.hip", "rq_gemm_fp6.hip", "rq_gemm_codebook.hip",
            "rq_gemm_mx.hip", "rq_trdq.hip", "rq_attn_api.cpp", "rq_qknorm.hip", "rq_attend.hip",
-           "rq_evict.hip"]
+           "rq_evict.hip", "rq_blocknorm.hip", "rq_rows.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 

@@ -23,14 +23,7 @@
 namespace rq {
 namespace {
 
-using attn::Cache;
-
-typedef float f4 __attribute__((ext_vector_type(4)));
-typedef float f2 __attribute__((ext_vector_type(2)));
-typedef __bf16 b8 __attribute__((ext_vector_type(8)));
-typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+using namespace attn;
 
 struct Args {
     Cache c;
@@ -68,12 +61,6 @@ constexpr int resident(int DP, bool plain, bool bf16) {   // plain: D == DP and 
     return DP == 256 ? 1 : DP == 128 ? (plain && bf16 ? 3 : 2) : 3;
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    const f2 v = {lo, hi};
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, b2));
-}
-__device__ __forceinline__ float lo_of(uint32_t p) { return __builtin_bit_cast(float, p << 16); }
-__device__ __forceinline__ float hi_of(uint32_t p) { return __builtin_bit_cast(float, p & 0xffff0000u); }
 __device__ __forceinline__ f4 mfma(u4 a, u4 b, f4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
 }
@@ -93,12 +80,6 @@ __device__ __forceinline__ u4 widen8(u2 c) {
 }
 // an offset past any row of scores (2^30 bytes), whose end does not wrap either
 constexpr int kNowhere = 0x7ffffff0;
-constexpr float kLn2 = 0.69314718055994531f;
-template <bool BF16>
-__device__ __forceinline__ void store4(void *p, int64_t at, f4 v) {
-    if constexpr (BF16) *reinterpret_cast<u2 *>(static_cast<uint16_t *>(p) + at) = u2{pack2(v[0], v[1]), pack2(v[2], v[3])};
-    else *reinterpret_cast<f4 *>(static_cast<float *>(p) + at) = v;
-}
 // t[j] = the bytes j of a, b, c, d
 __device__ __forceinline__ void turn4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&t)[4]) {
     const uint32_t ab = __builtin_amdgcn_perm(b, a, 0x05010400u), AB = __builtin_amdgcn_perm(b, a, 0x07030602u);
@@ -108,17 +89,6 @@ __device__ __forceinline__ void turn4(uint32_t a, uint32_t b, uint32_t c, uint32
     t[2] = __builtin_amdgcn_perm(CD, AB, 0x05040100u);
     t[3] = __builtin_amdgcn_perm(CD, AB, 0x07060302u);
 }
-// x as `parts` bf16 numbers whose sum carries 8 bits of x each
-template <int PARTS>
-__device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[PARTS]) {
-#pragma unroll
-    for (int i = 0; i < PARTS; ++i) {
-        p[i] = pack2(x, y);
-        x -= lo_of(p[i]);
-        y -= hi_of(p[i]);
-    }
-}
-
 __device__ __forceinline__ int length_of(const Args &a, int b) { return min(max(a.lens[b], 0), a.max_len); }
 __device__ __forceinline__ int steps_of(const Args &a, int len) { return (int)((uint32_t)(len + (1 << a.step_log) - 1) >> a.step_log); }
 
@@ -607,43 +577,6 @@ __global__ void __launch_bounds__(waves_of(DP, DIRECT) * 64) __attribute__((amdg
     }
     __syncthreads();
     }
-}
-
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float from_lane(float x, float none) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, x), CTRL, ROWS, 0xf, false));
-}
-// (shifts within rows of 16 lanes, then the rows' last lanes passed on: lane 63 has all)
-__device__ __forceinline__ float wave_max(float x) {
-    x = fmaxf(x, from_lane<0x111, 0xf>(x, -INFINITY));
-    x = fmaxf(x, from_lane<0x112, 0xf>(x, -INFINITY));
-    x = fmaxf(x, from_lane<0x114, 0xf>(x, -INFINITY));
-    x = fmaxf(x, from_lane<0x118, 0xf>(x, -INFINITY));
-    x = fmaxf(x, from_lane<0x142, 0xa>(x, -INFINITY));
-    x = fmaxf(x, from_lane<0x143, 0xc>(x, -INFINITY));
-    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
-}
-__device__ __forceinline__ float wave_sum(float x) {
-    x += from_lane<0x111, 0xf>(x, 0.0f);
-    x += from_lane<0x112, 0xf>(x, 0.0f);
-    x += from_lane<0x114, 0xf>(x, 0.0f);
-    x += from_lane<0x118, 0xf>(x, 0.0f);
-    x += from_lane<0x142, 0xa>(x, 0.0f);
-    x += from_lane<0x143, 0xc>(x, 0.0f);
-    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
-}
-// Statistics of a head over its n parts, by one wave: all lanes get the maximum
-// and the sum relative to it.
-__device__ __forceinline__ void join_stats(const f2 *st, int n, int stride, int lane, float &M, float &L) {
-    f2 mine = {-INFINITY, 0.0f};             // (a lane's own parts first)
-    for (int i = lane; i < n; i += 64) {
-        const f2 x = st[(int64_t)i * stride];
-        const float top = fmaxf(mine[0], x[0]);
-        if (top == -INFINITY) continue;
-        mine = f2{top, mine[1] * __builtin_amdgcn_exp2f(mine[0] - top) + x[1] * __builtin_amdgcn_exp2f(x[0] - top)};
-    }
-    M = wave_max(mine[0]);
-    L = wave_sum(mine[0] == -INFINITY ? 0.0f : mine[1] * __builtin_amdgcn_exp2f(mine[0] - M));
 }
 
 constexpr int kJoin = 256;     // threads of a joining workgroup

@@ -104,7 +104,7 @@ int launch_gemm_codebook(const uint8_t *codes, const uint8_t *codes_mma, const f
                          const rq_weight_header *hdr, const void *blob, const float *bias,
                          void *Y, int y_dtype, void *stream);
 
-// Attention around the linears (rq_qknorm.hip, rq_attend.hip, rq_evict.hip);
+// Around the linears (rq_qknorm.hip, rq_attend.hip, rq_evict.hip, rq_blocknorm.hip, rq_rows.hip);
 // arguments are validated by the caller (rq_attn_api.cpp).
 int launch_qk_norm_rope(const rq_qk_norm *d, const void *qkv, int bf16, int64_t ld, int64_t T,
                         const int32_t *positions, void *q_out, int64_t q_ld, void *k_out,
@@ -122,5 +122,21 @@ size_t evict_workspace_bytes(const rq_kv_cache *c, int keep, int64_t max_len);
 int launch_cache_evict(const rq_kv_cache *c, const int32_t *lens, int64_t max_len, int keep,
                        int recent, int sink, int32_t *lens_out, float *weight_out,
                        int32_t *pos_out, void *workspace, void *stream);
+// (x_bf16: x and h; io_bf16: y and z)
+int launch_block_norm(const rq_norm *post, const rq_norm *pre, const rq_modulation *mod, int width,
+                      const void *x, int x_bf16, int64_t x_ld, const void *y, int io_bf16, int64_t y_ld,
+                      int64_t T, float alpha, float beta, void *h, int64_t h_ld, void *z, int64_t z_ld,
+                      void *stream);
+bool cross_fits(const rq_states *s, int64_t queries, int q_heads, int bf16);
+size_t cross_workspace_bytes(const rq_states *s, int64_t queries, int q_heads, int bf16);
+int launch_cross_attention(const rq_states *s, const void *q, int bf16, int64_t q_ld, int64_t q_stride,
+                           int64_t queries, int q_heads, float scale, const int32_t *q_lens, void *out,
+                           int64_t out_ld, int64_t out_stride, float *lse, void *workspace, void *stream);
+bool prefix_fits(const rq_kv_cache *c, int q_heads, int bf16, int64_t prefix, int64_t max_len);
+size_t prefix_workspace_bytes(const rq_kv_cache *c, int q_heads, int bf16, int64_t prefix, int64_t max_len);
+int launch_prefix_attention(const rq_kv_cache *c, const int32_t *prefix_table, int64_t prefix, const void *q,
+                            int bf16, int64_t q_ld, int q_heads, float scale, const int32_t *lens,
+                            int64_t max_len, const uint8_t *mask, int64_t mask_ld, void *out, int64_t out_ld,
+                            float *lse, void *workspace, void *stream);
 
 }  // namespace rq

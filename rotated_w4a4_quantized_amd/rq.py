@@ -90,6 +90,25 @@ class c_qk_norm(ctypes.Structure):
                 ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p)]
 
 
+class c_norm(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p)]
+
+
+class c_modulation(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("reserved", ctypes.c_int32), ("ld", ctypes.c_int64),
+                ("per", ctypes.c_int64), ("index", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("shift", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class c_states(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("keys", ctypes.c_int64), ("k_ld", ctypes.c_int64),
+                ("v_ld", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("mask_ld", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("mask", ctypes.c_void_p)]
+
+
 # every symbol include/rq.h declares
 EXPORTS = ("rq_version", "rq_last_error", "rq_lloydmax_gaussian", "rq_packed_weight_bytes",
            "rq_pack_weights", "rq_rotate_quant_workspace_bytes", "rq_codes_mma_bytes",
@@ -97,7 +116,9 @@ EXPORTS = ("rq_version", "rq_last_error", "rq_lloydmax_gaussian", "rq_packed_wei
            "rq_rotate_quant_noalloc", "rq_activation_bytes", "rq_weight_set_bytes",
            "rq_pack_weight_set", "rq_weight_set_member", "rq_qk_norm_rope",
            "rq_paged_attention_workspace_bytes", "rq_paged_attention",
-           "rq_cache_evict_workspace_bytes", "rq_cache_evict")
+           "rq_cache_evict_workspace_bytes", "rq_cache_evict", "rq_block_norm",
+           "rq_cross_attention_workspace_bytes", "rq_cross_attention",
+           "rq_prefix_attention_workspace_bytes", "rq_prefix_attention")
 
 _lib = None
 
@@ -136,6 +157,12 @@ def load() -> ctypes.CDLL:
                                      P, I32, P, P, SZ, P]
     L.rq_cache_evict_workspace_bytes.argtypes = [P, I32, I64, ctypes.POINTER(SZ)]
     L.rq_cache_evict.argtypes = [P, P, I64, I32, I32, I32, P, P, P, P, SZ, P]
+    F = ctypes.c_float
+    L.rq_block_norm.argtypes = [P, P, P, I32, P, I32, I64, P, I32, I64, I64, F, F, P, I64, P, I64, P]
+    L.rq_cross_attention_workspace_bytes.argtypes = [P, I64, I32, I32, ctypes.POINTER(SZ)]
+    L.rq_cross_attention.argtypes = [P, P, I32, I64, I64, I64, I32, F, P, P, I64, I64, P, P, SZ, P]
+    L.rq_prefix_attention_workspace_bytes.argtypes = [P, I32, I32, I64, I64, ctypes.POINTER(SZ)]
+    L.rq_prefix_attention.argtypes = [P, P, I64, P, I32, I64, I32, F, P, I64, P, I64, P, I64, P, P, SZ, P]
     for name in ("rq_lloydmax_gaussian", "rq_packed_weight_bytes", "rq_pack_weights",
                  "rq_rotate_quant_workspace_bytes", "rq_codes_mma_bytes", "rq_rotate_quant",
                  "rq_w4a4_linear", "rq_w4a4_linear_engine", "rq_rotate_quant_noalloc",
@@ -756,3 +783,218 @@ def cache_evict(cache: KVCache, lens, keep, recent=0, sink=0, max_len=None, lens
         cache.c.weight if weight_out is None else _vector(weight_out, n, torch.float32, "weight_out"),
         cache.c.pos if pos_out is None else _vector(pos_out, n, torch.int32, "pos_out"),
         p_ws, ws_bytes, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# between the blocks; many queries to the same keys
+# ---------------------------------------------------------------------------
+
+NORMS = {"rms": 0, "layer": 1}
+
+
+class Norm:
+    """An RMS ("rms") or layer norm ("layer") over rows of `width` values, with
+    weight and bias fp32 [width] (None: ones, zeros)."""
+
+    def __init__(self, width, kind="rms", weight=None, bias=None, eps=1e-6):
+        import torch
+        if kind not in NORMS:
+            raise ValueError(f"kind must be one of {sorted(NORMS)}, got {kind!r}")
+        if weight is not None and bias is not None and weight.device != bias.device:
+            raise ValueError(f"weight and bias are on {weight.device} and {bias.device}")
+        self.width, self.weight, self.bias = width, weight, bias
+        self.c = c_norm(NORMS[kind], eps, _vector(weight, width, torch.float32, "weight"),
+                        _vector(bias, width, torch.float32, "bias"))
+        self._ref = ctypes.byref(self.c)
+
+
+class Modulation:
+    """What a conditioning network gives a block: gate, shift and scale, fp32
+    [rows][width] each or None, possibly parts of one wider tensor; token t
+    takes row index[t] (int32), or t // per (default: one row for all)."""
+
+    def __init__(self, gate=None, shift=None, scale=None, per=None, index=None):
+        import torch
+        held = [(n, t) for n, t in (("gate", gate), ("shift", shift), ("scale", scale)) if t is not None]
+        if not held:
+            raise ValueError("modulations need a gate, a shift or a scale")
+        rows, width = held[0][1].shape
+        ld = None
+        for n, t in held:
+            if t.dtype is not torch.float32 or t.dim() != 2 or t.shape != (rows, width) or (t.stride(1) != 1 and width > 1):
+                raise ValueError(f"{n} must be a float32 [rows][width] tensor of contiguous rows, all of one shape")
+            if t.device != held[0][1].device:
+                raise ValueError(f"{n} is on {t.device}, not on {held[0][1].device}")
+            if rows > 1:
+                if ld is not None and t.stride(0) != ld:
+                    raise ValueError("gate, shift and scale must have one stride from row to row")
+                ld = t.stride(0)
+        if index is not None and per is not None:
+            per = None   # (the index alone counts)
+        if index is not None and (index.dtype is not torch.int32 or index.dim() != 1 or not index.is_contiguous()):
+            raise ValueError("index must be a contiguous int32 [tokens] tensor")
+        if index is not None and index.device != held[0][1].device:
+            raise ValueError(f"index is on {index.device}, not on {held[0][1].device}")
+        self.gate, self.shift, self.scale, self.index = gate, shift, scale, index
+        self.rows, self.width = rows, width
+        ptr = (lambda t: None if t is None else t.data_ptr())
+        self.c = c_modulation(rows, 0, width if ld is None else ld, (1 << 62) if per is None else per, ptr(index),
+                              ptr(gate), ptr(shift), ptr(scale))
+        self._ref = ctypes.byref(self.c)
+        self._any = held[0][1]
+
+
+def block_norm(x, z=None, pre: Norm = None, y=None, post: Norm = None, h=None, mod: Modulation = None, alpha=1.0,
+               beta=1.0, stream=None):
+    """The residual stream between two blocks in one pass: h = alpha x + beta gate
+    post(y) and z = pre(h) (1 + scale) + shift, for rows x, h [T][width] of one
+    type and y, z of one (fp32 or bf16 each).  Leave out y (nothing is added), h
+    or z (not written).  h may be x itself, and z may be y."""
+    T, K = int(x.shape[0]), x.shape[-1]
+    io = y if y is not None else z
+    if x.dim() != 2:
+        raise ValueError("x must be rows [T][width]")
+    if h is not None and h.dtype is not x.dtype:
+        raise TypeError("h must have x's type")
+    if y is not None and z is not None and y.dtype is not z.dtype:
+        raise TypeError("z must have y's type")
+    for name, n in (("post", post), ("pre", pre)):
+        if n is not None and n.width != K:
+            raise ValueError(f"{name} is a norm of {n.width} values, the rows have {K}")
+    if mod is not None:
+        if mod.width != K:
+            raise ValueError(f"the modulations have {mod.width} values, the rows {K}")
+        if mod.index is not None and mod.index.numel() != T:
+            raise ValueError(f"index must have {T} elements, got {mod.index.numel()}")
+    _on_device(x.get_device(), y, h, z, None if mod is None else mod._any,
+               None if post is None else post.weight, None if post is None else post.bias,
+               None if pre is None else pre.weight, None if pre is None else pre.bias)
+    rows = (lambda t, name: (None, 0) if t is None else _rows(t, T, K, name))
+    p_x, x_ld = _rows(x, T, K, "x")
+    (p_y, y_ld), (p_h, h_ld), (p_z, z_ld) = rows(y, "y"), rows(h, "h"), rows(z, "z")
+    _check(load().rq_block_norm(
+        None if post is None else post._ref, None if pre is None else pre._ref, None if mod is None else mod._ref, K,
+        p_x, _io_dtype(x), x_ld, p_y, RQ_BF16 if io is None else _io_dtype(io), y_ld, T, alpha, beta, p_h, h_ld, p_z,
+        z_ld, _stream(stream)))
+
+
+def _tokens(t, name):
+    """Address, token stride and sequence stride of a [batch][tokens][heads][D]
+    tensor whose tokens' heads lie together."""
+    B, T, H, D = t.shape
+    s = t.stride()
+    if t.numel() == 0:
+        return t.data_ptr(), H * D, 0
+    if (s[3] != 1 and D > 1) or (s[2] != D and H > 1):
+        raise ValueError(f"the heads of a token of {name} must lie together")
+    # (single tokens and sequences have no stride to keep to)
+    return t.data_ptr(), s[1] if T > 1 else H * D, s[0] if B > 1 else 0
+
+
+class States:
+    """Keys and values of a batch, bf16 [batch][tokens][heads][D] (views of a
+    projection's output are fine; so is one sequence expanded over the batch),
+    with lens int32 [batch] and mask uint8 or bool [batch][tokens] (None: all
+    tokens count).  The tensors are held."""
+
+    def __init__(self, k, v, lens=None, mask=None):
+        import torch
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError("k and v must be [batch][tokens][heads][D] tensors of one shape")
+        if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16:
+            raise TypeError(f"k and v must be bfloat16, got {k.dtype} and {v.dtype}")
+        B, S, H, D = k.shape
+        for name, t in (("v", v), ("lens", lens), ("mask", mask)):
+            if t is not None and t.device != k.device:
+                raise ValueError(f"{name} is on {t.device}, not on {k.device}")
+        p_m, m_ld = None, 0
+        if mask is not None:
+            if mask.dtype not in (torch.uint8, torch.bool):
+                raise TypeError("mask must be uint8 or bool")
+            if mask.shape != (B, S) or (mask.stride(1) != 1 and S > 1):
+                raise ValueError(f"mask must be rows [{B}][{S}]")
+            p_m, m_ld = mask.data_ptr(), mask.stride(0) if B > 1 else S
+        (p_k, k_ld, k_b), (p_v, v_ld, v_b) = _tokens(k, "k"), _tokens(v, "v")
+        self.k, self.v, self.lens, self.mask = k, v, lens, mask
+        self.batch, self.keys, self.heads, self.head_dim = B, S, H, D
+        self.c = c_states(H, D, B, 0, S, k_ld, v_ld, k_b, v_b, m_ld, p_k, p_v,
+                          _vector(lens, B, torch.int32, "lens"), p_m)
+        self._ref = ctypes.byref(self.c)
+
+
+def _code(dtype) -> int:
+    import torch
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"expected torch.float32 or torch.bfloat16, got {dtype}")
+    return RQ_BF16 if dtype is torch.bfloat16 else RQ_F32
+
+
+def cross_attention_workspace_bytes(states: States, queries: int, q_heads: int, dtype) -> int:
+    """dtype: the queries' torch type."""
+    n = ctypes.c_size_t(0)
+    _check(load().rq_cross_attention_workspace_bytes(states._ref, queries, q_heads, _code(dtype), ctypes.byref(n)))
+    return n.value
+
+
+def cross_attention(q, states: States, out, scale=None, q_lens=None, lse=None, workspace=None, stream=None):
+    """Attention of q [batch][queries][q_heads][D] to its sequences' states
+    (softmax of scale, default 1 / sqrt(D), times the scores), to out of q's
+    shape and type; lse fp32 [batch][queries][q_heads].  Rows from q_lens[b]
+    (int32) on are left as they are."""
+    import torch
+    if q.dim() != 4 or q.shape != out.shape:
+        raise ValueError("q and out must be [batch][queries][heads][D] tensors of one shape")
+    if out.dtype is not q.dtype:
+        raise TypeError("out must have q's type")
+    B, T, H, D = q.shape
+    if B != states.batch or D != states.head_dim:
+        raise ValueError(f"q has {B} sequences of heads of {D}, the states {states.batch} of {states.head_dim}")
+    _on_device(q.get_device(), out, states.k, q_lens, lse, workspace)
+    (p_q, q_ld, q_b), (p_o, o_ld, o_b) = _tokens(q, "q"), _tokens(out, "out")
+    p_ws, ws_bytes = _workspace(workspace)
+    _check(load().rq_cross_attention(
+        states._ref, p_q, _io_dtype(q), q_ld, q_b, T, H, D ** -0.5 if scale is None else scale,
+        _vector(q_lens, B, torch.int32, "q_lens"), p_o, o_ld, o_b, _vector(lse, B * T * H, torch.float32, "lse"),
+        p_ws, ws_bytes, _stream(stream)))
+
+
+def prefix_attention_workspace_bytes(cache: KVCache, q_heads: int, prefix: int, max_len: int, dtype) -> int:
+    """dtype: the queries' torch type."""
+    n = ctypes.c_size_t(0)
+    _check(load().rq_prefix_attention_workspace_bytes(cache._ref, q_heads, _code(dtype), prefix, max_len, ctypes.byref(n)))
+    return n.value
+
+
+def prefix_attention(q, cache: KVCache, prefix_table, prefix, lens, out, scale=None, max_len=None, mask=None, lse=None,
+                     workspace=None, stream=None):
+    """paged_attention for a batch that shares its first `prefix` tokens, which
+    lie in the pages of prefix_table int32 [>= ceil(prefix / page)] and are read
+    once for all.  lens counts the prefix too; columns of mask below it are not
+    read.  A sequence shorter than the prefix gets 0."""
+    import torch
+    B, D = cache.batch, cache.head_dim
+    dt = _io_dtype(q)
+    if out.dtype is not q.dtype:
+        raise TypeError("out must have q's type")
+    width = q.shape[1] if q.dim() == 2 else q.shape[1] * q.shape[2]
+    if width % D:
+        raise ValueError(f"a row of q must be whole heads of {D}, got {width}")
+    _on_device(q.get_device(), cache.k, prefix_table, lens, out, mask, lse, workspace)
+    p_q, q_ld = _rows(q, B, width, "q")
+    p_o, o_ld = _rows(out, B, width, "out")
+    if max_len is None:
+        max_len = cache.slots
+    if prefix_table is not None:
+        n = -(-prefix // cache.page)
+        if prefix_table.dim() != 1 or prefix_table.numel() < n or prefix_table.dtype is not torch.int32 or not prefix_table.is_contiguous():
+            raise ValueError(f"prefix_table must be a contiguous int32 tensor of at least {n} pages")
+    p_m, m_ld = None, 0
+    if mask is not None:
+        if mask.dtype not in (torch.uint8, torch.bool):
+            raise TypeError("mask must be uint8 or bool")
+        p_m, m_ld = _rows(mask, B, max_len, "mask")
+    p_ws, ws_bytes = _workspace(workspace)
+    _check(load().rq_prefix_attention(
+        cache._ref, None if prefix_table is None or prefix == 0 else prefix_table.data_ptr(), prefix, p_q, dt, q_ld,
+        width // D, D ** -0.5 if scale is None else scale, _vector(lens, B, torch.int32, "lens"), max_len, p_m, m_ld,
+        p_o, o_ld, _vector(lse, B * (width // D), torch.float32, "lse"), p_ws, ws_bytes, _stream(stream)))
