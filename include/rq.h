@@ -866,7 +866,8 @@ rq_status rq_block_norm(const rq_norm *post, const rq_norm *pre, const rq_modula
  *   head_dim  D, 16 <= D <= 256, D % 8 == 0
  *   batch     sequences, 0 .. 65535
  *   keys      tokens of a sequence, 0 .. 2^24
- *   k_ld, v_ld          elements from token to token, >= heads * D, multiples of 8
+ *   k_ld, v_ld          elements from token to token, >= heads * D, at most 2^22,
+ *             multiples of 8
  *   k_stride, v_stride  elements from sequence to sequence, >= 0 (0: one for
  *             all), multiples of 8
  *   k, v      device bf16, 16-byte aligned

@@ -333,8 +333,10 @@ rq_status rq_cross_attention(const rq_states *states, const void *q, int32_t dty
         return fail(RQ_ERR_ALIGN, "rows of q and out must be 16-byte aligned");
     if (states->keys > 0) {
         if (!states->k || !states->v) return fail(RQ_ERR_NULL, "the states' k and v must not be NULL");
-        if (states->k_ld < kv || states->k_ld > wide || states->v_ld < kv || states->v_ld > wide)
-            return fail(RQ_ERR_SHAPE, "k_ld and v_ld must hold a row of heads * head_dim");
+        // (16 rows of at most 2^22 elements keep the offsets of one load below 2^31 bytes)
+        const int64_t most = int64_t(1) << 22;
+        if (states->k_ld < kv || states->k_ld > most || states->v_ld < kv || states->v_ld > most)
+            return fail(RQ_ERR_SHAPE, "k_ld and v_ld must hold a row of heads * head_dim, and 2^22 elements at most");
         if (states->k_stride < 0 || states->k_stride > far || states->v_stride < 0 || states->v_stride > far)
             return fail(RQ_ERR_SHAPE, "k_stride and v_stride must lie in [0, 2^46]");
         if (states->mask && states->mask_ld != 0 && (states->mask_ld < states->keys || states->mask_ld > wide))

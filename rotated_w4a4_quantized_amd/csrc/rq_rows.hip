@@ -54,14 +54,15 @@ struct Job {
     const int32_t *table;          // pages
     const uint8_t *mask;
     int h, R, row0;                // head; rows of the problem; first row of the tile
-    int begin, end;                // slots
+    int begin, end;                // slots; begin is a multiple of 16, and slots below first
+    int first;                     // do not count
     int64_t part, lse_at;          // part * rows of all + the problem's row 0; lse of token 0, head 0 of the group
 };
 
 __device__ __forceinline__ f16 mfma32(u4 a, u4 b, f16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
 }
-__device__ __forceinline__ u2 read_turned(const uint16_t *p) {
+__device__ __forceinline__ u2 read_turned(const char *p) {
     return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4 *)p));
 }
 // eight int8 codes -> eight bf16 (exact)
@@ -75,57 +76,207 @@ __device__ __forceinline__ u4 widen(u2 c) {
     return r;
 }
 
-// NB blocks of 32 rows a wave, RW waves along the rows, TW along the tokens of a step.
+// Pieces of 16 bytes (8 elements) of a token's row in LDS, as staged: without
+// padding (what a direct-to-LDS load writes is contiguous), but in another order in
+// each row, so that the lanes of one read fall on different banks.  K: 16 tokens'
+// same piece; V: 4 tokens' 4 neighbouring pieces.
+template <int PC>
+__device__ __forceinline__ int k_place(int row, int piece) {
+    return PC == 8 ? piece ^ (row >> 1 & 7) : PC == 12 ? piece ^ (row >> 2 & 3) : piece ^ (row & 15);
+}
+template <int PC>
+__device__ __forceinline__ int v_place(int row, int piece) {
+    return PC == 8 ? piece ^ ((row >> 1 & 1) * 4) : PC == 12 ? piece : piece ^ ((row & 3) * 4);
+}
+
+// 16 bytes a lane from base + offset to LDS byte at + 16 lane (buffer_load ... lds);
+// lanes with the offset kNowhere write zeros.  M0 holds the LDS address (saved and
+// restored: the compiler reserves it); completion is waited for by hand.
+constexpr uint32_t kNowhere = 0xc0000000u, kReach = 0x80000000u;
+__device__ __forceinline__ void to_lds(const char *base, uint32_t offset, uint32_t at) {
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    const u4 r = {(uint32_t)p, (uint32_t)(p >> 32) & 0xffffu, kReach, 0x00020000u};
+    uint32_t saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %3\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %1, %2, 0 offen lds\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "v"(offset), "s"(r), "s"(at)
+        : "memory");
+}
+
+// NB blocks of 32 rows a wave; RW waves along the rows, or TW along the tokens.
 template <int DP_, bool BF16_, int NB_, int RW_, int TW_, Source SRC_>
 struct Shape {
     static constexpr int DP = DP_, NB = NB_, RW = RW_, TW = TW_;
     static constexpr bool BF16 = BF16_;
     static constexpr Source SRC = SRC_;
-    static constexpr int threads = RW * TW * 64;
+    static constexpr int waves = RW * TW, threads = waves * 64;
     static constexpr int rows = RW * NB * 32;
     static constexpr int TB = TW == 1 ? 2 : 1;            // blocks of 32 tokens a wave takes in a step
     static constexpr int KT = TW * TB * 32;               // tokens of a step
-    static constexpr int KP = DP + 8, VP = DP + 16;       // elements from token to token in LDS: no two of the
-                                                          // eight rows that are read together share a bank
-    static constexpr int stage = KT * (KP + VP);          // elements of one buffer
-    static constexpr int scale_floats = SRC == PAGES_I8 ? 2 * KT : 0;
-    static constexpr size_t buffers = 2 * (stage * 2 + scale_floats * 4);
-    static constexpr int OP = DP + 4;                     // joining waves: floats from row to row
-    static constexpr size_t join = TW == 1 ? 0 : (size_t)TW * NB * 32 * (OP + 2) * 4;
-    static constexpr size_t lds = buffers > join ? buffers : join;
+    static constexpr int PC = DP / 8;                     // pieces of a row
+    static constexpr int half = KT * PC * 16;             // bytes of a step's keys
+    static constexpr int scales = SRC == PAGES_I8 ? 2 * KT * 4 : 0;
+    static constexpr int stage = 2 * half + scales;
+    // at the end: rows of results, or of the waves' parts
+    static constexpr int OP = DP + 4;                     // floats from row to row
+    static constexpr int ends = waves * NB * 32 * (OP * 4 + (TW > 1 ? 8 : 0));
+    static constexpr size_t lds = 2 * stage > ends ? 2 * stage : ends;
 };
 
-// A step of KT tokens goes through LDS (asked for a step ahead, in registers), and
-// each wave computes with v_mfma_f32_32x32x16_bf16
+// A step of KT tokens goes through LDS, one step ahead; each wave brings in its
+// share, bf16 straight from memory, int8 through registers, where it is widened.
+// A wave computes with v_mfma_f32_32x32x16_bf16
 //   S [token][row] = K Q^T: a lane gets, of row lane % 32, the tokens
-//     8 (i / 4) + 4 (lane / 32) + i % 4, i = 0 .. 15, of a block;
+//     8 (i / 4) + 4 (lane / 32) + i % 4, i = 0 .. 15, of a block of 32;
 //   O^T [d][row] = V^T P^T: the lane's weights are the operand as they lie, its k
 //     slots 8 (lane / 32) + e standing for the tokens above, and V^T is read in that
 //     order with the transposing LDS read.
+// Where the waves divide the tokens, each reads only what it brought in itself and
+// there is no barrier.
 //
 // Rounding: K, V and bf16 queries enter exactly, fp32 queries as three bf16 parts
 // (24 bits).  Weights enter as bf16 for bf16 outputs and as three bf16 parts for
 // fp32 ones; sums and statistics are fp32.
 template <class C>
 __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char *lds) {
-    constexpr int DP = C::DP, NB = C::NB, KT = C::KT, TB = C::TB;
-    constexpr bool BF16 = C::BF16, I8 = C::SRC == PAGES_I8, PAGED = C::SRC != STATES;
+    constexpr int DP = C::DP, NB = C::NB, KT = C::KT, TB = C::TB, PC = C::PC;
+    constexpr bool BF16 = C::BF16, I8 = C::SRC == PAGES_I8, PAGED = C::SRC != STATES, WIDE = C::TW == 1;
     constexpr int QP = BF16 ? 1 : 3;                  // parts of queries and weights
     constexpr int KS = DP / 16, DB = DP / 32;
-    constexpr int PIECES = DP / 8, N = KT * PIECES / C::threads;
-    static_assert(KT * PIECES % C::threads == 0, "whole pieces a thread");
-    constexpr int EB = I8 ? 1 : 2;
+    constexpr int BW = KT / 16 / C::waves;            // blocks of 16 tokens a wave brings in
+    constexpr int NI = PC / 4;                        // its loads a block, of K and of V
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int rw = wave / C::TW, tw = wave % C::TW;
     const int col = lane & 31, hf = lane >> 5;
     const int D = a.c.D, G = a.G;
+    const int own = WIDE ? 0 : wave * 32;             // first of the tokens of a step that the wave computes with
 
-    // rows and queries
+    // ---- bringing in
+    // slot j0 + own + lane: whether it counts, and its page, asked for two steps ahead
+    uint32_t use;
+    int32_t page_of = 0;
+    auto fetch = [&](int j0) {
+        const int j = j0 + own + lane, jj = min(max(j, job.first), job.end - 1);
+        use = job.mask ? job.mask[jj] : 1;
+        if (j != jj) use = 0;
+        if constexpr (PAGED) page_of = job.table[jj >> a.c.page_log];
+    };
+    auto settle = [&]() -> uint64_t {
+        if constexpr (PAGED)
+            if ((uint32_t)page_of >= (uint32_t)a.c.pages) use = 0, page_of = 0;
+        const uint64_t b = __ballot(use != 0);
+        return WIDE ? b : b & 0xffffffffull;
+    };
+    // the lane's pieces of a block: offsets of what lands at 16 lane of each load
+    uint32_t k_from[NI], v_from[NI];
+    const uint32_t k_row = PAGED ? D * 2 : (uint32_t)a.k_ld * 2, v_row = PAGED ? D * 2 : (uint32_t)a.v_ld * 2;
+    if constexpr (!I8)
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int s = i * 64 + lane, r = s / PC, kp = k_place<PC>(r, s % PC), vp = v_place<PC>(r, s % PC);
+            k_from[i] = kp * 8 < D ? r * k_row + kp * 16 : kNowhere;
+            v_from[i] = vp * 8 < D ? r * v_row + vp * 16 : kNowhere;
+        }
+    const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
+    const int page_mask = (1 << a.c.page_log) - 1;
+    auto bring = [&](int j0, uint64_t bits, int buf) {
+#pragma unroll
+        for (int b = 0; b < BW; ++b) {
+            const int block = wave * BW + b, in_bits = block * 16 - own, j = j0 + block * 16;
+            const char *kp, *vp;
+            if constexpr (PAGED) {
+                const int64_t pg = __builtin_amdgcn_readlane(page_of, in_bits);
+                const int64_t at = (((pg * a.c.heads + job.h) << a.c.page_log) + (j & page_mask)) * D * 2;
+                kp = static_cast<const char *>(a.c.k) + at;
+                vp = static_cast<const char *>(a.c.v) + at;
+            } else {
+                kp = job.k + j * a.k_ld * 2;
+                vp = job.v + j * a.v_ld * 2;
+            }
+            const uint32_t part = (uint32_t)(bits >> in_bits) & 0xffffu;
+            const uint32_t at = __builtin_amdgcn_readfirstlane(lds_at + buf * C::stage + block * 16 * PC * 16);
+            if (part == 0xffffu) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    to_lds(kp, k_from[i], at + i * 1024);
+                    to_lds(vp, v_from[i], at + C::half + i * 1024);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const bool in = (part >> ((i * 64 + lane) / PC) & 1) != 0;
+                    to_lds(kp, in ? k_from[i] : kNowhere, at + i * 1024);
+                    to_lds(vp, in ? v_from[i] : kNowhere, at + C::half + i * 1024);
+                }
+            }
+        }
+    };
+    // int8: the same through registers
+    constexpr int N = I8 ? BW * NI : 1, NS = I8 ? BW : 1;
+    u2 k_reg[N], v_reg[N];
+    float k_sc[NS], v_sc[NS];          // scales of slot block + lane % 16
+    auto load = [&](int j0) {
+        if constexpr (I8) {
+#pragma unroll
+            for (int b = 0; b < BW; ++b) {
+                const int block = wave * BW + b;
+                const int64_t pg = __builtin_amdgcn_readlane(page_of, block * 16 - own);
+                const int64_t at = ((pg * a.c.heads + job.h) << a.c.page_log) + ((j0 + block * 16) & page_mask);
+                const char *kp = static_cast<const char *>(a.c.k) + at * D, *vp = static_cast<const char *>(a.c.v) + at * D;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const int u = i * 64 + lane, t = u / PC, d = (u - t * PC) * 8;
+                    const uint32_t from = t * D + (d < D ? d : 0);
+                    k_reg[b * NI + i] = *reinterpret_cast<const u2 *>(kp + from);
+                    v_reg[b * NI + i] = *reinterpret_cast<const u2 *>(vp + from);
+                }
+                k_sc[b] = a.c.k_scale[at + lane % 16];
+                v_sc[b] = a.c.v_scale[at + lane % 16];
+            }
+        }
+    };
+    auto write = [&](uint64_t bits, int buf) {
+        if constexpr (I8) {
+            char *base = lds + buf * C::stage;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int u = i * 64 + lane, t = u / PC, p = u - t * PC, at = wave * BW * 16 + t;
+                const bool in = (bits >> (at - own) & 1) != 0 && p * 8 < D;
+                const u4 x = widen(k_reg[i]), y = widen(v_reg[i]);
+                *reinterpret_cast<u4 *>(base + (at * PC + k_place<PC>(at, p)) * 16) = in ? x : u4{0, 0, 0, 0};
+                *reinterpret_cast<u4 *>(base + C::half + (at * PC + v_place<PC>(at, p)) * 16) = in ? y : u4{0, 0, 0, 0};
+            }
+            if (lane < 16)
+#pragma unroll
+                for (int b = 0; b < BW; ++b) {
+                    const int at = (wave * BW + b) * 16 + lane;
+                    const bool in = (bits >> (at - own) & 1) != 0;
+                    float *sc = reinterpret_cast<float *>(base + 2 * C::half);
+                    sc[at] = in ? k_sc[b] : 0.0f;
+                    sc[KT + at] = in ? v_sc[b] : 0.0f;
+                }
+        }
+    };
+
+    uint64_t bits_next = 0;
+    if (job.begin < job.end) {
+        fetch(job.begin);
+        bits_next = settle();
+        if constexpr (I8) load(job.begin);
+        else bring(job.begin, bits_next, 0);
+        fetch(job.begin + KT);
+    }
+
+    // ---- rows and queries
     int row[NB];
     u4 q[NB][KS][QP];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-        row[nb] = job.row0 + (rw * NB + nb) * 32 + col;
+        row[nb] = job.row0 + ((WIDE ? wave * NB : 0) + nb) * 32 + col;
         const int r = min(row[nb], job.R - 1), t = r / G, g = r - t * G;
         const int64_t at = job.q_at + t * a.q_ld + (int64_t)(job.h * G + g) * D;
 #pragma unroll
@@ -173,107 +324,41 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
             for (int i = 0; i < 16; ++i) o[nb][db][i] = 0.0f;
     }
 
-    // ---- staging.  All loads leave under no condition (what lies outside reads some
-    // place inside), what must not count is cleared on the way to LDS.
-    constexpr int PG = (KT + 63) / 64;
-    int32_t page_of[PG];               // of slot j0 + 64 i + lane, a step ahead of the loads
-    u4 kreg[N], vreg[N];               // int8: the first two dwords
-    float ksreg = 0, vsreg = 0;        // int8: scales of slot j0 + thread
-    uint32_t use[PG];                  // slot j0 + 64 i + lane: whether it counts
-    const int page_mask = (1 << a.c.page_log) - 1;
-    auto load_pages = [&](int j0) {
+    // the lane's places in LDS, without the token block
+    int k_at[KS], v_at[DB];
 #pragma unroll
-        for (int i = 0; i < PG; ++i) page_of[i] = job.table[min(j0 + i * 64 + lane, job.end - 1) >> a.c.page_log];
-    };
-    auto load = [&](int j0) {
+    for (int ks = 0; ks < KS; ++ks) k_at[ks] = ((own + col) * PC + k_place<PC>(col, 2 * ks + hf)) * 16;
+    // (an address is the lane's part of the 4 tokens x 16 columns that 16 lanes turn)
+    const int v_row0 = own + 4 * hf + (lane >> 2 & 3);
 #pragma unroll
-        for (int i = 0; i < PG; ++i) {
-            const int j = j0 + i * 64 + lane, jj = min(j, job.end - 1);
-            use[i] = job.mask ? job.mask[jj] : 1;
-            if (j >= job.end) use[i] = 0;
-            if constexpr (PAGED) {
-                if ((uint32_t)page_of[i] >= (uint32_t)a.c.pages) use[i] = 0, page_of[i] = 0;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int u = i * C::threads + (int)threadIdx.x, t = u / PIECES, p = u - t * PIECES;
-            const int j = min(j0 + t, job.end - 1), d = p * 8 < D ? p * 8 : 0;
-            if constexpr (!PAGED) {
-                kreg[i] = *reinterpret_cast<const u4 *>(job.k + (j * a.k_ld + d) * 2);
-                vreg[i] = *reinterpret_cast<const u4 *>(job.v + (j * a.v_ld + d) * 2);
-            } else {
-                int32_t pg = __shfl(page_of[0], t & 63);
-                if constexpr (PG > 1) pg = t >= 64 ? __shfl(page_of[PG - 1], t & 63) : pg;
-                const int64_t r = (((int64_t)pg * a.c.heads + job.h) << a.c.page_log) + (j & page_mask);
-                const char *kp = static_cast<const char *>(a.c.k) + (r * D + d) * EB, *vp = static_cast<const char *>(a.c.v) + (r * D + d) * EB;
-                if constexpr (!I8) {
-                    kreg[i] = *reinterpret_cast<const u4 *>(kp);
-                    vreg[i] = *reinterpret_cast<const u4 *>(vp);
-                } else {
-                    const u2 x = *reinterpret_cast<const u2 *>(kp), y = *reinterpret_cast<const u2 *>(vp);
-                    kreg[i] = u4{x[0], x[1], 0, 0};
-                    vreg[i] = u4{y[0], y[1], 0, 0};
-                }
-            }
-        }
-        if constexpr (I8) {
-            const int t = threadIdx.x % KT, j = min(j0 + t, job.end - 1);
-            int32_t pg = __shfl(page_of[0], t & 63);
-            if constexpr (PG > 1) pg = t >= 64 ? __shfl(page_of[PG - 1], t & 63) : pg;
-            const int64_t r = (((int64_t)pg * a.c.heads + job.h) << a.c.page_log) + (j & page_mask);
-            ksreg = a.c.k_scale[r];
-            vsreg = a.c.v_scale[r];
-        }
-    };
-    uint64_t bits[PG];                 // which slots of a step count
-    auto stage = [&](int buf) {
-        uint16_t *kl = reinterpret_cast<uint16_t *>(lds) + buf * C::stage, *vl = kl + KT * C::KP;
-#pragma unroll
-        for (int i = 0; i < PG; ++i) bits[i] = __ballot(use[i] != 0);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int u = i * C::threads + (int)threadIdx.x, t = u / PIECES, p = u - t * PIECES;
-            uint64_t b = bits[0];
-            if constexpr (PG > 1) b = t >= 64 ? bits[PG - 1] : b;
-            const bool ok = (b >> (t & 63) & 1) != 0 && p * 8 < D;
-            u4 x = kreg[i], y = vreg[i];
-            if constexpr (I8) {
-                x = widen(u2{x[0], x[1]});
-                y = widen(u2{y[0], y[1]});
-            }
-            *reinterpret_cast<u4 *>(kl + t * C::KP + p * 8) = ok ? x : u4{0, 0, 0, 0};
-            *reinterpret_cast<u4 *>(vl + t * C::VP + p * 8) = ok ? y : u4{0, 0, 0, 0};
-        }
-        if constexpr (I8) {
-            float *sc = reinterpret_cast<float *>(lds + 2 * C::stage * 2) + buf * 2 * KT;
-            if (threadIdx.x < KT) {
-                const int t = threadIdx.x;
-                uint64_t b = bits[0];
-                if constexpr (PG > 1) b = t >= 64 ? bits[PG - 1] : b;
-                const bool ok = (b >> (t & 63) & 1) != 0;
-                sc[t] = ok ? ksreg : 0.0f;
-                sc[KT + t] = ok ? vsreg : 0.0f;
-            }
-        }
-    };
+    for (int db = 0; db < DB; ++db)
+        v_at[db] = C::half + (v_row0 * PC + v_place<PC>(v_row0, db * 4 + (lane >> 3 & 2) + (lane >> 1 & 1))) * 16 + (lane & 1) * 8;
 
-    if (job.begin < job.end) {
-        if constexpr (PAGED) load_pages(job.begin);
-        load(job.begin);
-        if constexpr (PAGED) load_pages(job.begin + KT);
-    }
     int buf = 0;
     for (int j0 = job.begin; j0 < job.end; j0 += KT, buf ^= 1) {
-        stage(buf);
-        if (j0 + KT < job.end) {
-            load(j0 + KT);
-            if constexpr (PAGED) load_pages(j0 + 2 * KT);
+        const uint64_t bits = bits_next;
+        const bool more = j0 + KT < job.end;
+        if constexpr (I8) {
+            // (the next write to this buffer is two steps away, behind the next step's barrier)
+            write(bits, buf);
+            if (more) {
+                bits_next = settle();
+                load(j0 + KT);
+                fetch(j0 + 2 * KT);
+            }
+            if constexpr (WIDE) __syncthreads();
+            else asm volatile("" ::: "memory");   // (a wave's LDS accesses keep their order)
+        } else {
+            // this step is here, and the other buffer is read no more
+            if constexpr (WIDE) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            if (more) {
+                bits_next = settle();
+                bring(j0 + KT, bits_next, buf ^ 1);
+                fetch(j0 + 2 * KT);
+            }
         }
-        // the next write to this buffer is two steps away, behind the next step's barrier
-        __syncthreads();
-        const uint16_t *kl = reinterpret_cast<const uint16_t *>(lds) + buf * C::stage, *vl = kl + KT * C::KP;
-        const int first = C::TW == 1 ? 0 : tw * 32;
+        const char *here = lds + buf * C::stage;
         f16 s[NB][TB];
 #pragma unroll
         for (int tb = 0; tb < TB; ++tb) {
@@ -283,7 +368,7 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
                 for (int i = 0; i < 16; ++i) s[nb][tb][i] = 0.0f;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                const u4 k = *reinterpret_cast<const u4 *>(kl + (first + tb * 32 + col) * C::KP + ks * 16 + hf * 8);
+                const u4 k = *reinterpret_cast<const u4 *>(here + k_at[ks] + tb * 32 * PC * 16);
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -291,38 +376,23 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
             }
         }
         // int8: the scales of the lane's tokens
-        float ksc[TB][16], vsc[TB][16];
-        if constexpr (I8) {
-            const float *sc = reinterpret_cast<const float *>(lds + 2 * C::stage * 2) + buf * 2 * KT + first + hf * 4;
+        const float *scales = reinterpret_cast<const float *>(here + 2 * C::half) + own + hf * 4;
+        if constexpr (I8)
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
-                    const f4 x = *reinterpret_cast<const f4 *>(sc + tb * 32 + i * 2), y = *reinterpret_cast<const f4 *>(sc + KT + tb * 32 + i * 2);
+                    const f4 x = *reinterpret_cast<const f4 *>(scales + tb * 32 + i * 2);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) ksc[tb][i + e] = x[e], vsc[tb][i + e] = y[e];
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[nb][tb][i + e] *= x[e];
                 }
-#pragma unroll
-            for (int tb = 0; tb < TB; ++tb)
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) s[nb][tb][i] *= ksc[tb][i];
-        }
         // slots that do not count
-        uint32_t mine[TB];
-        bool whole = true;
-#pragma unroll
-        for (int tb = 0; tb < TB; ++tb) {
-            uint64_t b = bits[0];
-            if constexpr (PG > 1) b = first + tb * 32 >= 64 ? bits[PG - 1] : b;
-            mine[tb] = (uint32_t)(b >> ((first + tb * 32) & 63));
-            whole = whole && mine[tb] == 0xffffffffu;
-        }
-        if (!whole) {
+        if (bits != (WIDE ? ~0ull : 0xffffffffull)) {
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb) {
-                const uint32_t b = mine[tb] >> (4 * hf);
+                const uint32_t b = (uint32_t)(bits >> (32 * tb)) >> (4 * hf);
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -340,7 +410,7 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[nb][tb][i]);
+                for (int i = 0; i < 16; i += 2) top = fmaxf(top, fmaxf(s[nb][tb][i], s[nb][tb][i + 1]));
             top *= a.scale2;
             if (__any(top > m[nb] + 8.0f)) {
                 top = fmaxf(fmaxf(top, __shfl_xor(top, 32)), m[nb]);
@@ -354,10 +424,15 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float p = __builtin_amdgcn_exp2f(fmaf(s[nb][tb][i], a.scale2, base));
-                    l[nb] += p;
-                    s[nb][tb][i] = I8 ? p * vsc[tb][i] : p;
+                for (int i = 0; i < 16; i += 4) {
+                    f4 x = {1, 1, 1, 1};
+                    if constexpr (I8) x = *reinterpret_cast<const f4 *>(scales + KT + tb * 32 + i * 2);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float p = __builtin_amdgcn_exp2f(fmaf(s[nb][tb][i + e], a.scale2, base));
+                        l[nb] += p;
+                        s[nb][tb][i + e] = I8 ? p * x[e] : p;
+                    }
                 }
         }
 #pragma unroll
@@ -374,11 +449,10 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
 #pragma unroll
                         for (int n = 0; n < QP; ++n) p[nb][n][i] = x[n];
                     }
-                // (a lane's address is its part of the 4 tokens x 16 columns that 16 lanes turn)
-                const uint16_t *vb = vl + (first + tb * 32 + half * 16 + 4 * hf + (lane & 15) / 4) * C::VP + (lane & 16) + (lane & 3) * 4;
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
-                    const u2 x = read_turned(vb + db * 32), y = read_turned(vb + 8 * C::VP + db * 32);
+                    const char *at = here + v_at[db] + (tb * 32 + half * 16) * PC * 16;
+                    const u2 x = read_turned(at), y = read_turned(at + 8 * PC * 16);
                     const u4 v = {x[0], x[1], y[0], y[1]};
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
@@ -388,19 +462,19 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
             }
     }
 
-    // ---- the end: o of lane (col, hf) is d = 32 db + 8 (i / 4) + 4 hf + i % 4 of its row
+    // ---- the end: o of lane (col, hf) is d = 32 db + 8 (i / 4) + 4 hf + i % 4 of its
+    // row; rows go through LDS, so that they are written whole
     const bool parts = a.part != nullptr;
-    auto put = [&](int r, int d, f4 x, float M, float L) {
-        if (parts) {
-            const int64_t at = job.part + r;
-            if (M != -INFINITY) *reinterpret_cast<f4 *>(a.part + at * D + d) = x;
-            if (d == 0) *reinterpret_cast<f2 *>(a.stat + at * 2) = f2{M, L};
-            return;
-        }
+    auto place_of = [&](int r) {           // of row r of the problem in out, elements
         const int t = r / G, g = r - t * G;
-        const float inv = M == -INFINITY ? 0.0f : 1.0f / L;
-        store4<BF16>(a.out, job.out_at + t * a.out_ld + (int64_t)(job.h * G + g) * D + d, x * inv);
-        if (d == 0 && a.lse) a.lse[job.lse_at + (int64_t)t * a.hq + g] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * kLn2;
+        return job.out_at + t * a.out_ld + (int64_t)(job.h * G + g) * D;
+    };
+    auto put_stat = [&](int r, float M, float L) {
+        if (parts) *reinterpret_cast<f2 *>(a.stat + (job.part + r) * 2) = f2{M, L};
+        else if (a.lse) {
+            const int t = r / G, g = r - t * G;
+            a.lse[job.lse_at + (int64_t)t * a.hq + g] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * kLn2;
+        }
     };
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
@@ -409,30 +483,55 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
         // through every join: exp2(inf - inf) is NaN, other parts count 0 beside it.
         if (l[nb] != l[nb]) m[nb] = INFINITY;
     }
-    if constexpr (C::TW == 1) {
+    __syncthreads();   // (the last step's LDS is read no more)
+    if constexpr (WIDE) {
+        constexpr bool H = BF16;               // rows of out in bf16, parts in fp32
+        constexpr int OP = C::OP;
+        char *mine = lds + wave * NB * 32 * OP * 4;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-            if (row[nb] < job.R)
+        for (int nb = 0; nb < NB; ++nb) {
+            const float f = parts ? 1.0f : m[nb] == -INFINITY ? 0.0f : 1.0f / l[nb];
+            if (hf == 0 && row[nb] < job.R) put_stat(row[nb], m[nb], l[nb]);
 #pragma unroll
-                for (int db = 0; db < DB; ++db)
+            for (int db = 0; db < DB; ++db)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int d = db * 32 + i * 8 + hf * 4;
-                        if (d < D) put(row[nb], d, f4{o[nb][db][4 * i], o[nb][db][4 * i + 1], o[nb][db][4 * i + 2], o[nb][db][4 * i + 3]}, m[nb], l[nb]);
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const int at = (nb * 32 + col) * OP + db * 32 + i * 8 + hf * 4;
+                    const f4 x = f4{o[nb][db][4 * i], o[nb][db][4 * i + 1], o[nb][db][4 * i + 2], o[nb][db][4 * i + 3]} * f;
+                    if (H && !parts) store4<true>(mine, at, x);
+                    else store4<false>(mine, at, x);
+                }
+        }
+        const int first = job.row0 + wave * NB * 32, n = min(NB * 32, job.R - first);   // (below 1: none)
+        if (H && !parts) {
+            const int pieces = D / 8;
+            for (int x = lane; x < n * pieces; x += 64) {
+                const int r = x / pieces, d = (x - r * pieces) * 8;
+                // (rows lie 8-byte aligned)
+                const u2 lo = *reinterpret_cast<const u2 *>(mine + (r * OP + d) * 2), hi = *reinterpret_cast<const u2 *>(mine + (r * OP + d) * 2 + 8);
+                *reinterpret_cast<u4 *>(static_cast<uint16_t *>(a.out) + place_of(first + r) + d) = u4{lo[0], lo[1], hi[0], hi[1]};
+            }
+        } else {
+            const int pieces = D / 4;
+            for (int x = lane; x < n * pieces; x += 64) {
+                const int r = x / pieces, d = (x - r * pieces) * 4;
+                const f4 v = *reinterpret_cast<const f4 *>(mine + (r * OP + d) * 4);
+                if (parts) *reinterpret_cast<f4 *>(a.part + (job.part + first + r) * D + d) = v;
+                else *reinterpret_cast<f4 *>(static_cast<float *>(a.out) + place_of(first + r) + d) = v;
+            }
+        }
     } else {
-        static_assert(C::TW == 1 || (NB == 1 && C::RW == 1), "waves along the tokens have the same 32 rows");
-        __syncthreads();   // (the last step's LDS is read no more)
+        static_assert(WIDE || (NB == 1 && C::RW == 1), "waves along the tokens have the same 32 rows");
         float *so = reinterpret_cast<float *>(lds), *st = so + C::TW * 32 * C::OP;
         if (hf == 0) {
-            st[(tw * 32 + col) * 2] = m[0];
-            st[(tw * 32 + col) * 2 + 1] = l[0];
+            st[(wave * 32 + col) * 2] = m[0];
+            st[(wave * 32 + col) * 2 + 1] = l[0];
         }
 #pragma unroll
         for (int db = 0; db < DB; ++db)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<f4 *>(so + (tw * 32 + col) * C::OP + db * 32 + i * 8 + hf * 4) =
+                *reinterpret_cast<f4 *>(so + (wave * 32 + col) * C::OP + db * 32 + i * 8 + hf * 4) =
                     f4{o[0][db][4 * i], o[0][db][4 * i + 1], o[0][db][4 * i + 2], o[0][db][4 * i + 3]};
         __syncthreads();
         const int rows = min(32, job.R - job.row0), quads = D / 4;
@@ -450,10 +549,16 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
                 L += st[(w * 32 + r) * 2 + 1] * f;
                 sum += *reinterpret_cast<const f4 *>(so + (w * 32 + r) * C::OP + d) * f;
             }
-            put(job.row0 + r, d, sum, M, L);
+            if (d == 0) put_stat(job.row0 + r, M, L);
+            if (parts) *reinterpret_cast<f4 *>(a.part + (job.part + job.row0 + r) * D + d) = sum;
+            else store4<BF16>(a.out, place_of(job.row0 + r) + d, sum * (M == -INFINITY ? 0.0f : 1.0f / L));
         }
     }
 }
+
+// waves of a SIMD, by the registers they need
+template <class C>
+constexpr int resident() { return C::BF16 && C::DP <= 128 && !(C::SRC == PAGES_I8 && C::TW > 1) ? 2 : 1; }
 
 // Keys of part `split`: equal shares in whole steps.
 __device__ __forceinline__ void share(int begin, int end, int splits, int split, int step, int &b, int &e) {
@@ -470,7 +575,7 @@ __device__ __forceinline__ int64_t job_of_block() {
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::threads) cross_kernel(Args a) {
+__global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu(resident<C>()))) cross_kernel(Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     int64_t id = job_of_block();
     const int tile = (int)(id % a.tiles);
@@ -486,6 +591,7 @@ __global__ void __launch_bounds__(C::threads) cross_kernel(Args a) {
     if (job.row0 >= job.R) return;
     const int keys = a.lens ? min(max(a.lens[b], 0), a.keys) : a.keys;
     share(0, keys, a.splits, split, C::KT, job.begin, job.end);
+    job.first = 0;
     job.q_at = b * a.q_stride;
     job.out_at = b * a.out_stride;
     job.k = static_cast<const char *>(a.k) + (b * a.k_stride + (int64_t)h * a.c.D) * 2;
@@ -500,7 +606,7 @@ __global__ void __launch_bounds__(C::threads) cross_kernel(Args a) {
 // The prefix (a problem a head, of all sequences' rows) and what each sequence
 // holds behind it (a problem a sequence and head).
 template <class C>
-__global__ void __launch_bounds__(C::threads) prefix_kernel(Args a) {
+__global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu(resident<C>()))) prefix_kernel(Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     int64_t id = job_of_block();
     Job job;
@@ -511,6 +617,7 @@ __global__ void __launch_bounds__(C::threads) prefix_kernel(Args a) {
     job.R = a.batch * a.G;
     job.row0 = tile * C::rows;
     share(0, a.prefix, a.splits, split, C::KT, job.begin, job.end);
+    job.first = 0;
     job.q_at = job.out_at = job.lse_at = 0;
     job.k = job.v = nullptr;
     job.table = a.prefix_table;
@@ -519,7 +626,7 @@ __global__ void __launch_bounds__(C::threads) prefix_kernel(Args a) {
     attend_rows<C>(a, job, lds);
 }
 template <class C>
-__global__ void __launch_bounds__(C::threads) own_kernel(Args a) {
+__global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu(resident<C>()))) own_kernel(Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     int64_t id = blockIdx.x;
     const int tiles = (a.G + C::rows - 1) / C::rows;
@@ -532,7 +639,9 @@ __global__ void __launch_bounds__(C::threads) own_kernel(Args a) {
     job.h = h;
     job.R = a.G;
     job.row0 = tile * C::rows;
-    share(a.prefix, max(a.prefix, min(a.lens[b], a.keys)), a.own_splits, split, C::KT, job.begin, job.end);
+    const int end = max(a.prefix, min(a.lens[b], a.keys));   // (its first 16 slots can begin below the prefix)
+    share(end > a.prefix ? a.prefix & ~15 : end, end, a.own_splits, split, C::KT, job.begin, job.end);
+    job.first = a.prefix;
     job.q_at = b * a.q_ld;
     job.out_at = job.lse_at = 0;
     job.k = job.v = nullptr;
@@ -586,10 +695,9 @@ __global__ void __launch_bounds__(kJoin) join_rows_kernel(Args a) {
 // The kernel's shape for a number of rows: many rows divide over the waves, few
 // leave the waves the tokens.
 constexpr int kNarrow = 32;
-int wide_nb(int DP, bool bf16) { return bf16 && DP <= 128 ? 2 : 1; }
 int narrow_waves(int DP) { return DP <= 128 ? 4 : 2; }
 int padded(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
-int rows_of(int DP, bool bf16, int64_t R) { return R <= kNarrow ? 32 : 128 * wide_nb(DP, bf16); }
+int rows_of(int64_t R) { return R <= kNarrow ? 32 : 128; }
 int step_of(int DP, int64_t R) { return R <= kNarrow ? narrow_waves(DP) * 32 : 64; }
 
 // Parts of a problem of `keys` where `jobs` workgroups take one each.
@@ -609,7 +717,7 @@ void by_dim(int DP, F f) {
 template <int DP, bool B, Source S>
 using Narrow = Shape<DP, B, 1, 1, DP <= 128 ? 4 : 2, S>;
 template <int DP, bool B, Source S>
-using Wide = Shape<DP, B, B && DP <= 128 ? 2 : 1, 4, 1, S>;
+using Wide = Shape<DP, B, 1, 4, 1, S>;
 
 template <class C>
 int go(void (*kern)(Args), int64_t grid, const Args &a, hipStream_t s) {
@@ -631,7 +739,7 @@ CrossPlan cross_plan(const rq_states *s, int64_t queries, int q_heads, bool bf16
     const int G = q_heads / s->heads;
     const int64_t R = queries * G;
     p.DP = padded(s->head_dim);
-    const int rows = rows_of(p.DP, bf16, R);
+    const int rows = rows_of(R);
     p.tiles = (int)((R + rows - 1) / rows);
     const int64_t jobs = (int64_t)p.tiles * s->heads * s->batch;
     p.splits = parts_of(jobs, s->keys, step_of(p.DP, R));
@@ -654,7 +762,7 @@ PrefixPlan prefix_plan(const rq_kv_cache *c, int q_heads, bool bf16, int64_t pre
     const int G = q_heads / c->heads;
     const int64_t R = (int64_t)c->batch * G;
     p.DP = padded(c->head_dim);
-    const int rows = rows_of(p.DP, bf16, R);
+    const int rows = rows_of(R);
     p.tiles = (int)((R + rows - 1) / rows);
     if (prefix > 0) p.splits = parts_of((int64_t)p.tiles * c->heads, prefix, step_of(p.DP, R));
     p.grid = (int64_t)p.tiles * c->heads * p.splits;
