@@ -86,10 +86,10 @@ __device__ __forceinline__ float wave_sum(float x) {
 }
 // Statistics of a head over its n parts, by one wave: all lanes get the maximum
 // and the sum relative to it.
-__device__ __forceinline__ void join_stats(const f2 *st, int n, int stride, int lane, float &M, float &L) {
+__device__ __forceinline__ void join_stats(const f2 *st, int n, int64_t stride, int lane, float &M, float &L) {
     f2 mine = {-INFINITY, 0.0f};             // (a lane's own parts first)
     for (int i = lane; i < n; i += 64) {
-        const f2 x = st[(int64_t)i * stride];
+        const f2 x = st[i * stride];
         const float top = fmaxf(mine[0], x[0]);
         if (top == -INFINITY) continue;
         mine = f2{top, mine[1] * __builtin_amdgcn_exp2f(mine[0] - top) + x[1] * __builtin_amdgcn_exp2f(x[0] - top)};

@@ -392,7 +392,8 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
         if (bits != (WIDE ? ~0ull : 0xffffffffull)) {
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb) {
-                const uint32_t b = (uint32_t)(bits >> (32 * tb)) >> (4 * hf);
+                uint32_t b = (uint32_t)(bits >> (32 * tb)) >> (4 * hf);
+                asm volatile("" : "+v"(b));   // (else all steps would compute the choice)
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -410,7 +411,7 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) top = fmaxf(top, fmaxf(s[nb][tb][i], s[nb][tb][i + 1]));
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[nb][tb][i]);
             top *= a.scale2;
             if (__any(top > m[nb] + 8.0f)) {
                 top = fmaxf(fmaxf(top, __shfl_xor(top, 32)), m[nb]);
@@ -569,20 +570,21 @@ __device__ __forceinline__ void share(int begin, int end, int splits, int split,
 
 // Workgroups go round the 8 XCDs in turn; consecutive jobs, which share keys, are
 // given to the same one.
-__device__ __forceinline__ int64_t job_of_block() {
-    const int64_t n = gridDim.x, id = blockIdx.x, each = n / 8, more = n % 8, x = id % 8;
+__device__ __forceinline__ uint32_t job_of_block() {
+    const uint32_t n = gridDim.x, id = blockIdx.x, each = n / 8, more = n % 8, x = id % 8;
     return x * each + min(x, more) + id / 8;
 }
 
 template <class C>
 __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu(resident<C>()))) cross_kernel(Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    int64_t id = job_of_block();
-    const int tile = (int)(id % a.tiles);
+    // (sequences innermost: their lengths differ, and each XCD gets some of all)
+    uint32_t id = job_of_block();
+    const int b = id % a.batch;
+    id /= a.batch;
+    const int tile = id % a.tiles;
     id /= a.tiles;
-    const int split = (int)(id % a.splits);
-    id /= a.splits;
-    const int h = (int)(id % a.c.heads), b = (int)(id / a.c.heads);
+    const int split = id % a.splits, h = id / a.splits;
     Job job;
     job.h = h;
     const int queries = a.q_lens ? min(max(a.q_lens[b], 0), a.queries) : a.queries;
@@ -608,12 +610,12 @@ __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu
 template <class C>
 __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu(resident<C>()))) prefix_kernel(Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    int64_t id = job_of_block();
+    uint32_t id = job_of_block();
     Job job;
-    const int tile = (int)(id % a.tiles);
+    const int tile = id % a.tiles;
     id /= a.tiles;
-    const int split = (int)(id % a.splits);
-    job.h = (int)(id / a.splits);
+    const int split = id % a.splits;
+    job.h = id / a.splits;
     job.R = a.batch * a.G;
     job.row0 = tile * C::rows;
     share(0, a.prefix, a.splits, split, C::KT, job.begin, job.end);
@@ -628,13 +630,13 @@ __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu
 template <class C>
 __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu(resident<C>()))) own_kernel(Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    int64_t id = blockIdx.x;
+    uint32_t id = blockIdx.x;
     const int tiles = (a.G + C::rows - 1) / C::rows;
-    const int tile = (int)(id % tiles);
+    const int tile = id % tiles;
     id /= tiles;
-    const int split = (int)(id % a.own_splits);
+    const int split = id % a.own_splits;
     id /= a.own_splits;
-    const int h = (int)(id % a.c.heads), b = (int)(id / a.c.heads);
+    const int h = id % a.c.heads, b = id / a.c.heads;
     Job job;
     job.h = h;
     job.R = a.G;
@@ -676,16 +678,20 @@ __global__ void __launch_bounds__(kJoin) join_rows_kernel(Args a) {
         lse_at = ((int64_t)b * a.queries + t) * a.hq + h * a.G + g;
     }
     const f2 *st = reinterpret_cast<const f2 *>(a.stat) + row;
-    float M = -INFINITY, L = 0.0f;
-    for (int i = lane; i < n; i += 64) M = fmaxf(M, st[i * a.rows][0]);
-    M = wave_max(M);
+    float M, L;
+    join_stats(st, n, a.rows, lane, M, L);
     f4 sum = {0, 0, 0, 0};
-    for (int i = 0; i < n; ++i) {
-        const f2 x = st[i * a.rows];
-        if (x[0] == -INFINITY) continue;
-        const float f = __builtin_amdgcn_exp2f(x[0] - M);
-        L += x[1] * f;
-        if (lane < D / 4) sum += *reinterpret_cast<const f4 *>(a.part + (i * a.rows + row) * D + lane * 4) * f;
+    const float *part = a.part + row * D + min(lane, D / 4 - 1) * 4;
+    for (int i0 = 0; i0 < n; i0 += 64) {
+        // (a part without keys holds zeros)
+        const int mine = min(i0 + lane, n - 1), here = min(64, n - i0);
+        const float m = st[(int64_t)mine * a.rows][0];
+        const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - M);
+        // (no branch on the lane: all lanes' factors are read)
+#pragma unroll 8
+        for (int i = 0; i < here; ++i)
+            sum += *reinterpret_cast<const f4 *>(part + (int64_t)(i0 + i) * a.rows * D) *
+                   __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), i));
     }
     const float inv = M == -INFINITY ? 0.0f : 1.0f / L;
     if (lane < D / 4) store4<BF16>(a.out, out_at + lane * 4, sum * inv);
