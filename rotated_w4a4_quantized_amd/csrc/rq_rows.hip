@@ -27,6 +27,20 @@ typedef short s4 __attribute__((ext_vector_type(4)));
 // where keys and values come from
 enum Source { STATES, PAGES, PAGES_I8 };
 
+// Division by a number that the host knows: n / d for n < 2^30, d <= 2^30.
+// (With 2^shift <= d < 2^(shift + 1) and magic = ceil(2^(31 + shift) / d) the
+// product is over by less than n d / 2^(31 + shift) < 1 parts of d.)
+struct Over {
+    uint32_t d, magic, shift;
+    __device__ __forceinline__ int of(int n) const { return (int)(__umulhi(2u * (uint32_t)n, magic) >> shift); }
+};
+Over over(int64_t d) {
+    Over x{(uint32_t)d, 0, 0};
+    while ((int64_t(2) << x.shift) <= d) ++x.shift;
+    x.magic = (uint32_t)(((uint64_t(1) << (31 + x.shift)) + d - 1) / d);
+    return x;
+}
+
 struct Args {
     Cache c;                       // pages (heads, D: always)
     const void *k, *v;             // states
@@ -43,6 +57,7 @@ struct Args {
     int64_t rows;                  // rows of all problems: batch * heads * queries * G
     int32_t batch, queries, keys, hq, G;
     int32_t tiles, splits;         // row tiles and parts of a problem
+    Over by_G, by_batch, by_tiles, by_splits;
     int32_t prefix, own_splits;    // shared prefix
     float scale2, q_factor;        // |scale| * log2(e); the queries' sign (0 with scale 0)
 };
@@ -56,6 +71,8 @@ struct Job {
     int h, R, row0;                // head; rows of the problem; first row of the tile
     int begin, end;                // slots; begin is a multiple of 16, and slots below first
     int first;                     // do not count
+    int others;                    // parts of these rows that join (part: of the first of them)
+    bool to_parts;
     int64_t part, lse_at;          // part * rows of all + the problem's row 0; lse of token 0, head 0 of the group
 };
 
@@ -108,6 +125,8 @@ __device__ __forceinline__ void to_lds(const char *base, uint32_t offset, uint32
         : "memory");
 }
 
+constexpr int kOthers = 64;   // parts of a problem, at most
+
 // NB blocks of 32 rows a wave; RW waves along the rows, or TW along the tokens.
 template <int DP_, bool BF16_, int NB_, int RW_, int TW_, Source SRC_>
 struct Shape {
@@ -122,10 +141,11 @@ struct Shape {
     static constexpr int half = KT * PC * 16;             // bytes of a step's keys
     static constexpr int scales = SRC == PAGES_I8 ? 2 * KT * 4 : 0;
     static constexpr int stage = 2 * half + scales;
+    static constexpr int bias = waves * 64 * 4;           // behind the two buffers: what each wave leaves out
     // at the end: rows of results, or of the waves' parts
     static constexpr int OP = DP + 4;                     // floats from row to row
-    static constexpr int ends = waves * NB * 32 * (OP * 4 + (TW > 1 ? 8 : 0));
-    static constexpr size_t lds = 2 * stage > ends ? 2 * stage : ends;
+    static constexpr int ends = waves * NB * 32 * (OP * 4 + (TW > 1 ? 8 : 0)) + (TW > 1 ? kOthers * 256 + 256 : 0);
+    static constexpr size_t lds = 2 * stage + bias > ends ? 2 * stage + bias : ends;
 };
 
 // A step of KT tokens goes through LDS, one step ahead; each wave brings in its
@@ -256,7 +276,7 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
                     const int at = (wave * BW + b) * 16 + lane;
                     const bool in = (bits >> (at - own) & 1) != 0;
                     float *sc = reinterpret_cast<float *>(base + 2 * C::half);
-                    sc[at] = in ? k_sc[b] : 0.0f;
+                    sc[at] = in ? k_sc[b] : 1.0f;   // (times -infinity)
                     sc[KT + at] = in ? v_sc[b] : 0.0f;
                 }
         }
@@ -277,23 +297,22 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
         row[nb] = job.row0 + ((WIDE ? wave * NB : 0) + nb) * 32 + col;
-        const int r = min(row[nb], job.R - 1), t = r / G, g = r - t * G;
+        const int r = min(row[nb], job.R - 1), t = a.by_G.of(r), g = r - t * G;
         const int64_t at = job.q_at + t * a.q_ld + (int64_t)(job.h * G + g) * D;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            const int d = ks * 16 + hf * 8;
-            const bool in = d < D;
+            // (past D: any of the row, K is zero there)
+            const int d = ks * 16 + hf * 8 < D ? ks * 16 + hf * 8 : 0;
             if constexpr (BF16) {
-                const u4 x = *reinterpret_cast<const u4 *>(static_cast<const uint16_t *>(a.q) + at + (in ? d : 0));
-                q[nb][ks][0] = in ? x : u4{0, 0, 0, 0};
+                q[nb][ks][0] = *reinterpret_cast<const u4 *>(static_cast<const uint16_t *>(a.q) + at + d);
             } else {
-                const float *p = static_cast<const float *>(a.q) + at + (in ? d : 0);
+                const float *p = static_cast<const float *>(a.q) + at + d;
                 const f4 x = *reinterpret_cast<const f4 *>(p), y = *reinterpret_cast<const f4 *>(p + 4);
                 const float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t p3[3];
-                    split2<3>(in ? z[2 * i] : 0.0f, in ? z[2 * i + 1] : 0.0f, p3);
+                    split2<3>(z[2 * i], z[2 * i + 1], p3);
 #pragma unroll
                     for (int n = 0; n < QP; ++n) q[nb][ks][n][i] = p3[n];
                 }
@@ -360,20 +379,41 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
         }
         const char *here = lds + buf * C::stage;
         f16 s[NB][TB];
+        auto scores = [&](auto from) {
 #pragma unroll
-        for (int tb = 0; tb < TB; ++tb) {
+            for (int tb = 0; tb < TB; ++tb) {
+                from(tb);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+                for (int ks = 0; ks < KS; ++ks) {
+                    const u4 k = *reinterpret_cast<const u4 *>(here + k_at[ks] + tb * 32 * PC * 16);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s[nb][tb][i] = 0.0f;
+                    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const u4 k = *reinterpret_cast<const u4 *>(here + k_at[ks] + tb * 32 * PC * 16);
+                        for (int n = 0; n < QP; ++n) s[nb][tb] = mfma32(k, q[nb][ks][n], s[nb][tb]);
+                }
+            }
+        };
+        if (bits == (WIDE ? ~0ull : 0xffffffffull)) {
+            scores([&](int tb) {
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int n = 0; n < QP; ++n) s[nb][tb] = mfma32(k, q[nb][ks][n], s[nb][tb]);
-            }
+                    for (int i = 0; i < 16; ++i) s[nb][tb][i] = 0.0f;
+            });
+        } else {
+            // slots that do not count start from -infinity (their keys are zeros)
+            float *bias = reinterpret_cast<float *>(lds + 2 * C::stage) + wave * 64;
+            bias[lane] = (bits >> lane & 1) != 0 ? 0.0f : -INFINITY;
+            scores([&](int tb) {
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const f4 x = *reinterpret_cast<const f4 *>(bias + tb * 32 + i * 2 + hf * 4);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[nb][tb][i + e] = x[e];
+                }
+            });
         }
         // int8: the scales of the lane's tokens
         const float *scales = reinterpret_cast<const float *>(here + 2 * C::half) + own + hf * 4;
@@ -388,21 +428,6 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
 #pragma unroll
                         for (int e = 0; e < 4; ++e) s[nb][tb][i + e] *= x[e];
                 }
-        // slots that do not count
-        if (bits != (WIDE ? ~0ull : 0xffffffffull)) {
-#pragma unroll
-            for (int tb = 0; tb < TB; ++tb) {
-                uint32_t b = (uint32_t)(bits >> (32 * tb)) >> (4 * hf);
-                asm volatile("" : "+v"(b));   // (else all steps would compute the choice)
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float x = s[nb][tb][i];
-                        s[nb][tb][i] = (b >> (8 * (i / 4) + i % 4) & 1) ? x : -INFINITY;
-                    }
-            }
-        }
         // The running maximum only moves when a score passes it by 2^8: weights up to
         // 256 are as exact, and most steps leave the sums as they are.
 #pragma unroll
@@ -417,9 +442,11 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
                 top = fmaxf(fmaxf(top, __shfl_xor(top, 32)), m[nb]);
                 const float f = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[nb] - top);
                 m[nb] = top;
-                l[nb] *= f;
+                if (j0 != job.begin) {   // (zeros so far)
+                    l[nb] *= f;
 #pragma unroll
-                for (int db = 0; db < DB; ++db) o[nb][db] *= f;
+                    for (int db = 0; db < DB; ++db) o[nb][db] *= f;
+                }
             }
             const float base = m[nb] == -INFINITY ? 0.0f : -m[nb];
 #pragma unroll
@@ -465,16 +492,16 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
 
     // ---- the end: o of lane (col, hf) is d = 32 db + 8 (i / 4) + 4 hf + i % 4 of its
     // row; rows go through LDS, so that they are written whole
-    const bool parts = a.part != nullptr;
+    const bool parts = job.to_parts;
     auto place_of = [&](int r) {           // of row r of the problem in out, elements
-        const int t = r / G, g = r - t * G;
+        const int t = a.by_G.of(r), g = r - t * G;
         return job.out_at + t * a.out_ld + (int64_t)(job.h * G + g) * D;
     };
     auto put_stat = [&](int r, float M, float L) {
         if (parts) *reinterpret_cast<f2 *>(a.stat + (job.part + r) * 2) = f2{M, L};
         else if (a.lse) {
-            const int t = r / G, g = r - t * G;
-            a.lse[job.lse_at + (int64_t)t * a.hq + g] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * kLn2;
+            const int t = a.by_G.of(r), g = r - t * G;
+            a.lse[job.lse_at + (int64_t)t * a.hq + g] = M == -INFINITY ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
         }
     };
 #pragma unroll
@@ -491,7 +518,7 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
         char *mine = lds + wave * NB * 32 * OP * 4;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const float f = parts ? 1.0f : m[nb] == -INFINITY ? 0.0f : 1.0f / l[nb];
+            const float f = parts ? 1.0f : m[nb] == -INFINITY ? 0.0f : BF16 ? __builtin_amdgcn_rcpf(l[nb]) : 1.0f / l[nb];
             if (hf == 0 && row[nb] < job.R) put_stat(row[nb], m[nb], l[nb]);
 #pragma unroll
             for (int db = 0; db < DB; ++db)
@@ -505,17 +532,17 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
         }
         const int first = job.row0 + wave * NB * 32, n = min(NB * 32, job.R - first);   // (below 1: none)
         if (H && !parts) {
-            const int pieces = D / 8;
-            for (int x = lane; x < n * pieces; x += 64) {
-                const int r = x / pieces, d = (x - r * pieces) * 8;
+            for (int x = lane; x < n * PC; x += 64) {
+                const int r = x / PC, d = (x - r * PC) * 8;
+                if (d >= D) continue;
                 // (rows lie 8-byte aligned)
                 const u2 lo = *reinterpret_cast<const u2 *>(mine + (r * OP + d) * 2), hi = *reinterpret_cast<const u2 *>(mine + (r * OP + d) * 2 + 8);
                 *reinterpret_cast<u4 *>(static_cast<uint16_t *>(a.out) + place_of(first + r) + d) = u4{lo[0], lo[1], hi[0], hi[1]};
             }
         } else {
-            const int pieces = D / 4;
-            for (int x = lane; x < n * pieces; x += 64) {
-                const int r = x / pieces, d = (x - r * pieces) * 4;
+            for (int x = lane; x < n * (DP / 4); x += 64) {
+                const int r = x / (DP / 4), d = (x - r * (DP / 4)) * 4;
+                if (d >= D) continue;
                 const f4 v = *reinterpret_cast<const f4 *>(mine + (r * OP + d) * 4);
                 if (parts) *reinterpret_cast<f4 *>(a.part + (job.part + first + r) * D + d) = v;
                 else *reinterpret_cast<f4 *>(static_cast<float *>(a.out) + place_of(first + r) + d) = v;
@@ -535,21 +562,48 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
                 *reinterpret_cast<f4 *>(so + (wave * 32 + col) * C::OP + db * 32 + i * 8 + hf * 4) =
                     f4{o[0][db][4 * i], o[0][db][4 * i + 1], o[0][db][4 * i + 2], o[0][db][4 * i + 3]};
         __syncthreads();
-        const int rows = min(32, job.R - job.row0), quads = D / 4;
-        for (int x = threadIdx.x; x < rows * quads; x += C::threads) {
-            const int r = x / quads, d = (x - r * quads) * 4;
+        const int rows = min(32, job.R - job.row0);
+        // Parts that another launch left for these rows join here: their maxima, sums
+        // and then factors lie behind the waves' own.
+        const int others = job.others;
+        f2 *ot = reinterpret_cast<f2 *>(st + C::TW * 64);
+        float *fin = st + C::TW * 64 + kOthers * 64;    // [32][2]: maximum and sum of all
+        for (int x = threadIdx.x; x < rows * others; x += C::threads) {
+            const int i = x / rows, r = x - i * rows;
+            ot[i * 32 + r] = reinterpret_cast<const f2 *>(a.stat)[i * a.rows + job.part + job.row0 + r];
+        }
+        if (others) __syncthreads();
+        if ((int)threadIdx.x < rows) {
+            const int r = threadIdx.x;
             float M = -INFINITY, L = 0.0f;
 #pragma unroll
             for (int w = 0; w < C::TW; ++w) M = fmaxf(M, st[(w * 32 + r) * 2]);
+            for (int i = 0; i < others; ++i) M = fmaxf(M, ot[i * 32 + r][0]);
+            auto part_of = [&](float mw, float lw) {
+                const float f = mw == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mw - M);
+                if (mw != -INFINITY) L += lw * f;
+                return f;
+            };
+#pragma unroll
+            for (int w = 0; w < C::TW; ++w) st[(w * 32 + r) * 2] = part_of(st[(w * 32 + r) * 2], st[(w * 32 + r) * 2 + 1]);
+            for (int i = 0; i < others; ++i) {
+                const f2 x = ot[i * 32 + r];
+                ot[i * 32 + r] = f2{part_of(x[0], x[1]), 0.0f};
+            }
+            fin[r * 2] = M;
+            fin[r * 2 + 1] = L;
+        }
+        __syncthreads();
+        for (int x = threadIdx.x; x < rows * (DP / 4); x += C::threads) {
+            const int r = x / (DP / 4), d = (x - r * (DP / 4)) * 4;
+            if (d >= D) continue;
+            const float M = fin[r * 2], L = fin[r * 2 + 1];
             f4 sum = {0, 0, 0, 0};
 #pragma unroll
-            for (int w = 0; w < C::TW; ++w) {
-                const float mw = st[(w * 32 + r) * 2];
-                if (mw == -INFINITY) continue;
-                const float f = __builtin_amdgcn_exp2f(mw - M);
-                L += st[(w * 32 + r) * 2 + 1] * f;
-                sum += *reinterpret_cast<const f4 *>(so + (w * 32 + r) * C::OP + d) * f;
-            }
+            for (int w = 0; w < C::TW; ++w) sum += *reinterpret_cast<const f4 *>(so + (w * 32 + r) * C::OP + d) * st[(w * 32 + r) * 2];
+            const float *other = a.part + (job.part + job.row0 + r) * D + d;
+#pragma unroll 8
+            for (int i = 0; i < others; ++i) sum += *reinterpret_cast<const f4 *>(other + i * a.rows * D) * ot[i * 32 + r][0];
             if (d == 0) put_stat(job.row0 + r, M, L);
             if (parts) *reinterpret_cast<f4 *>(a.part + (job.part + job.row0 + r) * D + d) = sum;
             else store4<BF16>(a.out, place_of(job.row0 + r) + d, sum * (M == -INFINITY ? 0.0f : 1.0f / L));
@@ -579,13 +633,10 @@ template <class C>
 __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu(resident<C>()))) cross_kernel(Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     // (sequences innermost: their lengths differ, and each XCD gets some of all)
-    uint32_t id = job_of_block();
-    const int b = id % a.batch;
-    id /= a.batch;
-    const int tile = id % a.tiles;
-    id /= a.tiles;
-    const int split = id % a.splits, h = id / a.splits;
+    const int id = job_of_block(), id1 = a.by_batch.of(id), id2 = a.by_tiles.of(id1), h = a.by_splits.of(id2);
+    const int b = id - id1 * a.batch, tile = id1 - id2 * a.tiles, split = id2 - h * a.splits;
     Job job;
+    job.others = 0, job.to_parts = a.splits > 1;
     job.h = h;
     const int queries = a.q_lens ? min(max(a.q_lens[b], 0), a.queries) : a.queries;
     job.R = queries * a.G;
@@ -606,16 +657,16 @@ __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu
 }
 
 // The prefix (a problem a head, of all sequences' rows) and what each sequence
-// holds behind it (a problem a sequence and head).
+// holds behind it (a problem a sequence and head), which joins the prefix's parts
+// unless it has several itself.
 template <class C>
 __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu(resident<C>()))) prefix_kernel(Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    uint32_t id = job_of_block();
+    const int id = job_of_block(), id2 = a.by_tiles.of(id), tile = id - id2 * a.tiles;
     Job job;
-    const int tile = id % a.tiles;
-    id /= a.tiles;
-    const int split = id % a.splits;
-    job.h = id / a.splits;
+    job.h = a.by_splits.of(id2);
+    job.others = 0, job.to_parts = true;
+    const int split = id2 - job.h * a.splits;
     job.R = a.batch * a.G;
     job.row0 = tile * C::rows;
     share(0, a.prefix, a.splits, split, C::KT, job.begin, job.end);
@@ -630,49 +681,56 @@ __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu
 template <class C>
 __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu(resident<C>()))) own_kernel(Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    uint32_t id = blockIdx.x;
     const int tiles = (a.G + C::rows - 1) / C::rows;
+    uint32_t id = blockIdx.x;
     const int tile = id % tiles;
     id /= tiles;
-    const int split = id % a.own_splits;
-    id /= a.own_splits;
+    const int split = id % max(a.own_splits, 1);
+    id /= max(a.own_splits, 1);
     const int h = id % a.c.heads, b = id / a.c.heads;
     Job job;
     job.h = h;
     job.R = a.G;
     job.row0 = tile * C::rows;
-    const int end = max(a.prefix, min(a.lens[b], a.keys));   // (its first 16 slots can begin below the prefix)
-    share(end > a.prefix ? a.prefix & ~15 : end, end, a.own_splits, split, C::KT, job.begin, job.end);
+    const int len = min(a.lens[b], a.keys);
+    const bool there = len >= a.prefix && len > 0;           // else it is not in the batch
+    const int end = there ? len : a.prefix;                  // (its first 16 slots can begin below the prefix)
+    share(end > a.prefix ? a.prefix & ~15 : end, end, max(a.own_splits, 1), split, C::KT, job.begin, job.end);
     job.first = a.prefix;
     job.q_at = b * a.q_ld;
-    job.out_at = job.lse_at = 0;
+    job.out_at = b * a.out_ld;
+    job.lse_at = (int64_t)b * a.hq + h * a.G;
     job.k = job.v = nullptr;
     job.table = a.c.table + (int64_t)b * a.c.table_ld;
     job.mask = a.mask ? a.mask + b * a.mask_ld : nullptr;
-    job.part = (a.splits + split) * a.rows + ((int64_t)h * a.batch + b) * a.G;
+    job.part = ((int64_t)h * a.batch + b) * a.G;
+    job.to_parts = a.own_splits > 1;
+    job.others = job.to_parts || !there ? 0 : a.splits;
+    if (job.to_parts) job.part += (a.splits + split) * a.rows;
     attend_rows<C>(a, job, lds);
 }
 
 constexpr int kJoin = 256;
 
-// Joins the parts of a row, a wave a row.
-template <bool BF16, bool PREFIX>
+// Joins the parts of rows, TPR threads a row: a wave where there are many rows, a
+// workgroup where there are few.
+template <bool BF16, bool PREFIX, int TPR>
 __global__ void __launch_bounds__(kJoin) join_rows_kernel(Args a) {
-    const int lane = threadIdx.x & 63, D = a.c.D;
-    const int64_t row = (int64_t)blockIdx.x * (kJoin / 64) + (threadIdx.x >> 6);
-    if (row >= a.rows) return;
+    __shared__ float s_f[kJoin / TPR][2 * kOthers];
+    __shared__ f4 s_o[TPR == 64 ? 1 : kJoin];
+    const int lane = threadIdx.x & 63, D = a.c.D, quads = D / 4, t0 = threadIdx.x % TPR;
+    const int64_t row = (int64_t)blockIdx.x * (kJoin / TPR) + threadIdx.x / TPR;
+    if (row >= a.rows) return;   // (whole waves; a workgroup a row: none)
     int n = a.splits + a.own_splits;
     int64_t out_at, lse_at;
     if constexpr (PREFIX) {
-        const int64_t hb = row / a.G;
-        const int g = (int)(row - hb * a.G), h = (int)(hb / a.batch), b = (int)(hb - (int64_t)h * a.batch);
+        const int hb = a.by_G.of((int)row), g = (int)row - hb * a.G, h = a.by_batch.of(hb), b = hb - h * a.batch;
         if (min(a.lens[b], a.keys) < a.prefix || a.lens[b] <= 0) n = 0;   // not in the batch
         out_at = b * a.out_ld + (int64_t)(h * a.G + g) * D;
         lse_at = (int64_t)b * a.hq + h * a.G + g;
     } else {
-        const int64_t rows = (int64_t)a.queries * a.G, bh = row / rows;
-        const int r = (int)(row - bh * rows), t = r / a.G, g = r - t * a.G;
-        const int b = (int)(bh / a.c.heads), h = (int)(bh - (int64_t)b * a.c.heads);
+        const int tg = a.by_G.of((int)row), g = (int)row - tg * a.G;
+        const int bh = tg / a.queries, t = tg - bh * a.queries, b = bh / a.c.heads, h = bh - b * a.c.heads;
         if (a.q_lens && t >= a.q_lens[b]) return;
         out_at = b * a.out_stride + t * a.out_ld + (int64_t)(h * a.G + g) * D;
         lse_at = ((int64_t)b * a.queries + t) * a.hq + h * a.G + g;
@@ -680,22 +738,46 @@ __global__ void __launch_bounds__(kJoin) join_rows_kernel(Args a) {
     const f2 *st = reinterpret_cast<const f2 *>(a.stat) + row;
     float M, L;
     join_stats(st, n, a.rows, lane, M, L);
+    float *f = s_f[threadIdx.x / TPR];
+    for (int i = t0; i < n; i += TPR) {   // (a part without keys holds zeros)
+        const float m = st[i * a.rows][0];
+        f[i] = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - M);
+    }
+    if constexpr (TPR > 64) __syncthreads();
+    // the threads of a row take its quads, several parts at a time
+    const int groups = TPR / quads, group = t0 / quads, d = (t0 - group * quads) * 4;
     f4 sum = {0, 0, 0, 0};
-    const float *part = a.part + row * D + min(lane, D / 4 - 1) * 4;
-    for (int i0 = 0; i0 < n; i0 += 64) {
-        // (a part without keys holds zeros)
-        const int mine = min(i0 + lane, n - 1), here = min(64, n - i0);
-        const float m = st[(int64_t)mine * a.rows][0];
-        const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - M);
-        // (no branch on the lane: all lanes' factors are read)
+    if (group < groups) {
+        const float *part = a.part + row * D + d;
 #pragma unroll 8
-        for (int i = 0; i < here; ++i)
-            sum += *reinterpret_cast<const f4 *>(part + (int64_t)(i0 + i) * a.rows * D) *
-                   __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), i));
+        for (int i = group; i < n; i += groups) sum += *reinterpret_cast<const f4 *>(part + i * a.rows * D) * f[i];
+    }
+    if constexpr (TPR > 64) {
+        s_o[threadIdx.x] = sum;
+        __syncthreads();
+        if (t0 < quads)
+            for (int g = 1; g < groups; ++g) sum += s_o[t0 + g * quads];
+    } else {
+        // (groups are runs of lanes)
+        const f4 own = sum;
+        for (int g = 1; g < groups; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = own[e];
+                sum[e] += __shfl(x, (lane + g * quads) & 63);
+            }
     }
     const float inv = M == -INFINITY ? 0.0f : 1.0f / L;
-    if (lane < D / 4) store4<BF16>(a.out, out_at + lane * 4, sum * inv);
-    if (lane == 0 && a.lse) a.lse[lse_at] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * kLn2;
+    if (t0 < quads) store4<BF16>(a.out, out_at + d, sum * inv);
+    if (t0 == 0 && a.lse) a.lse[lse_at] = M == -INFINITY ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
+}
+
+template <bool BF16, bool PREFIX>
+void join(const Args &a, hipStream_t s) {
+    if (a.rows >= 8 * device_cus())
+        hipLaunchKernelGGL((join_rows_kernel<BF16, PREFIX, 64>), dim3((unsigned)((a.rows + 3) / 4)), dim3(kJoin), 0, s, a);
+    else
+        hipLaunchKernelGGL((join_rows_kernel<BF16, PREFIX, kJoin>), dim3((unsigned)a.rows), dim3(kJoin), 0, s, a);
 }
 
 // The kernel's shape for a number of rows: many rows divide over the waves, few
@@ -707,10 +789,10 @@ int rows_of(int64_t R) { return R <= kNarrow ? 32 : 128; }
 int step_of(int DP, int64_t R) { return R <= kNarrow ? narrow_waves(DP) * 32 : 64; }
 
 // Parts of a problem of `keys` where `jobs` workgroups take one each.
-int parts_of(int64_t jobs, int64_t keys, int step) {
+int parts_of(int64_t jobs, int64_t keys, int step, int least) {
     const int64_t steps = (keys + step - 1) / step, most = 2 * device_cus();
     if (jobs >= device_cus() || jobs < 1) return 1;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({steps, most / jobs, 64}));
+    return (int)std::max<int64_t>(1, std::min<int64_t>({steps / least, most / jobs, kOthers}));
 }
 
 template <class F>
@@ -748,7 +830,7 @@ CrossPlan cross_plan(const rq_states *s, int64_t queries, int q_heads, bool bf16
     const int rows = rows_of(R);
     p.tiles = (int)((R + rows - 1) / rows);
     const int64_t jobs = (int64_t)p.tiles * s->heads * s->batch;
-    p.splits = parts_of(jobs, s->keys, step_of(p.DP, R));
+    p.splits = parts_of(jobs, s->keys, step_of(p.DP, R), 4);
     p.grid = jobs * p.splits;
     p.rows = R * s->heads * s->batch;
     if (p.splits > 1) {
@@ -770,13 +852,13 @@ PrefixPlan prefix_plan(const rq_kv_cache *c, int q_heads, bool bf16, int64_t pre
     p.DP = padded(c->head_dim);
     const int rows = rows_of(R);
     p.tiles = (int)((R + rows - 1) / rows);
-    if (prefix > 0) p.splits = parts_of((int64_t)p.tiles * c->heads, prefix, step_of(p.DP, R));
+    if (prefix > 0) p.splits = parts_of((int64_t)p.tiles * c->heads, prefix, step_of(p.DP, R), 1);
     p.grid = (int64_t)p.tiles * c->heads * p.splits;
     const int own_tiles = (G + 31) / 32;
-    if (max_len > prefix) p.own_splits = parts_of((int64_t)own_tiles * c->heads * c->batch, max_len - prefix, step_of(p.DP, 1));
+    p.own_splits = parts_of((int64_t)own_tiles * c->heads * c->batch, max_len - prefix, step_of(p.DP, 1), 4);
     p.own_grid = (int64_t)own_tiles * c->heads * c->batch * p.own_splits;
     p.rows = R * c->heads;
-    const int parts = p.splits + p.own_splits;
+    const int parts = p.splits + (p.own_splits > 1 ? p.own_splits : 0);
     p.part = round16((size_t)parts * p.rows * c->head_dim * 4);
     p.stat = round16((size_t)parts * p.rows * 8);
     return p;
@@ -811,6 +893,7 @@ int launch_cross_attention(const rq_states *st, const void *q, int bf16, int64_t
     a.out = out, a.out_ld = out_ld, a.out_stride = out_stride, a.lse = lse;
     a.batch = st->batch, a.hq = q_heads, a.G = q_heads / st->heads;
     a.tiles = p.tiles, a.splits = p.splits, a.rows = p.rows;
+    a.by_G = over(a.G), a.by_batch = over(a.batch), a.by_tiles = over(a.tiles), a.by_splits = over(a.splits);
     set_scale(a, scale);
     if (p.splits > 1) {
         a.part = static_cast<float *>(workspace);
@@ -826,9 +909,7 @@ int launch_cross_attention(const rq_states *st, const void *q, int bf16, int64_t
     };
     by_dim(p.DP, [&](auto dp) { bf16 ? run(dp, std::true_type{}) : run(dp, std::false_type{}); });
     if (err != 0) return err;
-    if (p.splits > 1)
-        hipLaunchKernelGGL((bf16 ? join_rows_kernel<true, false> : join_rows_kernel<false, false>),
-                           dim3((unsigned)((p.rows + kJoin / 64 - 1) / (kJoin / 64))), dim3(kJoin), 0, s, a);
+    if (p.splits > 1) bf16 ? join<true, false>(a, s) : join<false, false>(a, s);
     return (int)hipGetLastError();
 }
 
@@ -853,6 +934,7 @@ int launch_prefix_attention(const rq_kv_cache *c, const int32_t *prefix_table, i
     a.batch = c->batch, a.hq = q_heads, a.G = q_heads / c->heads;
     a.tiles = p.tiles, a.splits = p.splits, a.own_splits = p.own_splits, a.rows = p.rows;
     a.prefix = (int)prefix, a.prefix_table = prefix_table;
+    a.by_G = over(a.G), a.by_batch = over(a.batch), a.by_tiles = over(a.tiles), a.by_splits = over(std::max(a.splits, 1));
     set_scale(a, scale);
     a.part = static_cast<float *>(workspace);
     a.stat = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.part);
@@ -868,7 +950,7 @@ int launch_prefix_attention(const rq_kv_cache *c, const int32_t *prefix_table, i
             if ((int64_t)a.batch * a.G <= kNarrow) err = go<N>(prefix_kernel<N>, p.grid, a, s);
             else err = go<W>(prefix_kernel<W>, p.grid, a, s);
         }
-        if (err == 0 && p.own_grid > 0) err = go<N>(own_kernel<N>, p.own_grid, a, s);
+        if (err == 0) err = go<N>(own_kernel<N>, p.own_grid, a, s);
     };
     by_dim(p.DP, [&](auto dp) {
         auto typed = [&](auto b) {
@@ -878,8 +960,7 @@ int launch_prefix_attention(const rq_kv_cache *c, const int32_t *prefix_table, i
         bf16 ? typed(std::true_type{}) : typed(std::false_type{});
     });
     if (err != 0) return err;
-    hipLaunchKernelGGL((bf16 ? join_rows_kernel<true, true> : join_rows_kernel<false, true>),
-                       dim3((unsigned)((p.rows + kJoin / 64 - 1) / (kJoin / 64))), dim3(kJoin), 0, s, a);
+    if (p.own_splits > 1) bf16 ? join<true, true>(a, s) : join<false, true>(a, s);
     return (int)hipGetLastError();
 }
 
