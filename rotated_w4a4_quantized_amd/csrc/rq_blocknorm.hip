@@ -76,10 +76,10 @@ __device__ __forceinline__ void store8(void *p, int64_t at, const float (&f)[8])
 // always the same channels, so that the modulations stay in registers while the
 // tokens walk by.  RB, IB: x and h, y and z are bf16 (else fp32).
 template <bool RB, bool IB, int WAVES, int CH>
-__global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) block_norm_kernel(Args a) {
+__global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) __attribute__((amdgpu_waves_per_eu(2))) block_norm_kernel(Args a) {
     constexpr int GROUPS = WAVES == 1 ? 4 : 1;   // tokens of a workgroup at a time
     __shared__ float s_sum[2][WAVES];
-    const int lane = threadIdx.x % (WAVES * 64), wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x % (WAVES * 64), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t group = (int64_t)blockIdx.x * GROUPS + (WAVES == 1 ? wave : 0);
     const int64_t t0 = group * a.run;
     if (t0 >= a.T) return;   // (whole waves; with WAVES > 1 whole workgroups)

@@ -369,8 +369,11 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
             else asm volatile("" ::: "memory");   // (a wave's LDS accesses keep their order)
         } else {
             // this step is here, and the other buffer is read no more
-            if constexpr (WIDE) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            // (vmcnt(0); by the builtin, so that the compiler knows that the queries are here,
+            // too: in the loop it would wait for them behind the loads of the next step)
+            __builtin_amdgcn_s_waitcnt(0xf70);
+            if constexpr (WIDE) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            else asm volatile("" ::: "memory");
             if (more) {
                 bits_next = settle();
                 bring(j0 + KT, bits_next, buf ^ 1);
@@ -379,17 +382,26 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
         }
         const char *here = lds + buf * C::stage;
         f16 s[NB][TB];
+        // Reads leave a block of products ahead (left to itself, the compiler has each
+        // product wait for its own).
         auto scores = [&](auto from) {
+            u4 k[2][KS];
+            auto read_k = [&](int tb, int ks) { k[tb & 1][ks] = *reinterpret_cast<const u4 *>(here + k_at[ks] + tb * 32 * PC * 16); };
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) read_k(0, ks);
 #pragma unroll
             for (int tb = 0; tb < TB; ++tb) {
                 from(tb);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    const u4 k = *reinterpret_cast<const u4 *>(here + k_at[ks] + tb * 32 * PC * 16);
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                        for (int n = 0; n < QP; ++n) s[nb][tb] = mfma32(k, q[nb][ks][n], s[nb][tb]);
+                        for (int n = 0; n < QP; ++n) s[nb][tb] = mfma32(k[tb & 1][ks], q[nb][ks][n], s[nb][tb]);
+                    if (tb + 1 < TB) read_k(tb + 1, ks);
+                    // (at 96 the order costs registers that a third wave needs)
+                    if (DP != 96) __builtin_amdgcn_sched_barrier(0);
                 }
             }
         };
@@ -448,46 +460,57 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
                     for (int db = 0; db < DB; ++db) o[nb][db] *= f;
                 }
             }
-            const float base = m[nb] == -INFINITY ? 0.0f : -m[nb];
-#pragma unroll
-            for (int tb = 0; tb < TB; ++tb)
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    f4 x = {1, 1, 1, 1};
-                    if constexpr (I8) x = *reinterpret_cast<const f4 *>(scales + KT + tb * 32 + i * 2);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float p = __builtin_amdgcn_exp2f(fmaf(s[nb][tb][i + e], a.scale2, base));
-                        l[nb] += p;
-                        s[nb][tb][i + e] = I8 ? p * x[e] : p;
-                    }
-                }
         }
+        // Group g of 16 slots: its weights are computed between the products of the
+        // group before, and its values read there.
+        constexpr int GROUPS = TB * 2;
+        float base[NB];
 #pragma unroll
-        for (int tb = 0; tb < TB; ++tb)
+        for (int nb = 0; nb < NB; ++nb) base[nb] = m[nb] == -INFINITY ? 0.0f : -m[nb];
+        u4 v[2][DB], p[2][NB][QP];
+        auto read_v = [&](int g, int db) {
+            const char *at = here + v_at[db] + g * 16 * PC * 16;
+            const u2 x = read_turned(at), y = read_turned(at + 8 * PC * 16);
+            v[g & 1][db] = u4{x[0], x[1], y[0], y[1]};
+        };
+        auto weigh = [&](int g, int i) {   // two weights
+            const int tb = g / 2, e = g % 2 * 8 + i * 2;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                u4 p[NB][QP];
+            for (int nb = 0; nb < NB; ++nb) {
+                float w0 = __builtin_amdgcn_exp2f(fmaf(s[nb][tb][e], a.scale2, base[nb]));
+                float w1 = __builtin_amdgcn_exp2f(fmaf(s[nb][tb][e + 1], a.scale2, base[nb]));
+                l[nb] += w0 + w1;
+                if constexpr (I8) {
+                    const f2 x = *reinterpret_cast<const f2 *>(scales + KT + tb * 32 + (e / 4) * 8 + e % 4);
+                    w0 *= x[0], w1 *= x[1];
+                }
+                uint32_t x[QP];
+                split2<QP>(w0, w1, x);
+#pragma unroll
+                for (int n = 0; n < QP; ++n) p[g & 1][nb][n][i] = x[n];
+            }
+        };
+#pragma unroll
+        for (int db = 0; db < DB; ++db) read_v(0, db);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) weigh(0, i);
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+            for (int db = 0; db < DB; ++db) {
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t x[QP];
-                        split2<QP>(s[nb][tb][half * 8 + 2 * i], s[nb][tb][half * 8 + 2 * i + 1], x);
+                    for (int n = 0; n < QP; ++n) o[nb][db] = mfma32(v[g & 1][db], p[g & 1][nb][n], o[nb][db]);
+                if (g + 1 < GROUPS) {
+                    read_v(g + 1, db);
 #pragma unroll
-                        for (int n = 0; n < QP; ++n) p[nb][n][i] = x[n];
-                    }
-#pragma unroll
-                for (int db = 0; db < DB; ++db) {
-                    const char *at = here + v_at[db] + (tb * 32 + half * 16) * PC * 16;
-                    const u2 x = read_turned(at), y = read_turned(at + 8 * PC * 16);
-                    const u4 v = {x[0], x[1], y[0], y[1]};
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int n = 0; n < QP; ++n) o[nb][db] = mfma32(v, p[nb][n], o[nb][db]);
+                    for (int i = db * 4 / DB; i < (db + 1) * 4 / DB; ++i) weigh(g + 1, i);
                 }
             }
+        __builtin_amdgcn_sched_barrier(0);
     }
 
     // ---- the end: o of lane (col, hf) is d = 32 db + 8 (i / 4) + 4 hf + i % 4 of its
@@ -613,7 +636,10 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
 
 // waves of a SIMD, by the registers they need
 template <class C>
-constexpr int resident() { return C::BF16 && C::DP <= 128 && !(C::SRC == PAGES_I8 && C::TW > 1) ? 2 : 1; }
+constexpr int resident() {
+    if (C::SRC == PAGES_I8) return C::BF16 && C::DP <= 128 && C::TW == 1 ? 2 : 1;
+    return C::BF16 && C::DP <= 128 ? (C::DP == 96 ? 3 : 2) : 1;
+}
 
 // Keys of part `split`: equal shares in whole steps.
 __device__ __forceinline__ void share(int begin, int end, int splits, int split, int step, int &b, int &e) {
@@ -632,9 +658,11 @@ __device__ __forceinline__ uint32_t job_of_block() {
 template <class C>
 __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu(resident<C>()))) cross_kernel(Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    // (sequences innermost: their lengths differ, and each XCD gets some of all)
+    // Sequences innermost: their lengths differ, and each XCD gets some of all.  They
+    // take turns in being first, or those of one length would meet on the same CUs.
     const int id = job_of_block(), id1 = a.by_batch.of(id), id2 = a.by_tiles.of(id1), h = a.by_splits.of(id2);
-    const int b = id - id1 * a.batch, tile = id1 - id2 * a.tiles, split = id2 - h * a.splits;
+    const int turn = id - id1 * a.batch + id1 % a.batch, b = turn < a.batch ? turn : turn - a.batch;
+    const int tile = id1 - id2 * a.tiles, split = id2 - h * a.splits;
     Job job;
     job.others = 0, job.to_parts = a.splits > 1;
     job.h = h;
