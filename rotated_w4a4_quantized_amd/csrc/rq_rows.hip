@@ -106,24 +106,71 @@ __device__ __forceinline__ int v_place(int row, int piece) {
     return PC == 8 ? piece ^ ((row >> 1 & 1) * 4) : PC == 12 ? piece : piece ^ ((row & 3) * 4);
 }
 
-// 16 bytes a lane from base + offset to LDS byte at + 16 lane (buffer_load ... lds);
-// lanes with the offset kNowhere write zeros.  M0 holds the LDS address (saved and
-// restored: the compiler reserves it); completion is waited for by hand.
+// A block of 16 tokens' keys and values to LDS, N loads of 16 bytes a lane each
+// (buffer_load ... lds): load i of the keys takes base k + k_from[i], and lane l's
+// bytes land at `at` + 1024 i + 16 l; the values `apart` behind.  Lanes with the
+// offset kNowhere write zeros.  M0 holds the LDS address (saved and restored: the
+// compiler reserves it; one wait state after writing it); completion is waited for
+// by hand.  One piece of assembly: each load as a piece of its own took five scalar
+// instructions more, and a wave spent a third of a step's time on them.
 constexpr uint32_t kNowhere = 0xc0000000u, kReach = 0x80000000u;
-__device__ __forceinline__ void to_lds(const char *base, uint32_t offset, uint32_t at) {
-    const uint64_t p = reinterpret_cast<uint64_t>(base);
-    const u4 r = {(uint32_t)p, (uint32_t)(p >> 32) & 0xffffu, kReach, 0x00020000u};
+#define RQ_LOAD(from, base) "buffer_load_dwordx4 %[" from "], %[" base "], 0 offen lds\n\t"
+#define RQ_NEXT "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+#define RQ_BEGIN "s_mov_b32 %[saved], m0\n\ts_mov_b32 m0, %[at]\n\ts_nop 0\n\t"
+#define RQ_VALUES "s_add_u32 m0, %[at], %[apart]\n\ts_nop 0\n\t"
+#define RQ_END "s_mov_b32 m0, %[saved]"
+template <int N>
+__device__ __forceinline__ void to_lds(const char *k, const char *v, const uint32_t (&k_from)[N], const uint32_t (&v_from)[N],
+                                       uint32_t at, uint32_t apart) {
+    const uint64_t pk = reinterpret_cast<uint64_t>(k), pv = reinterpret_cast<uint64_t>(v);
+    const u4 rk = {(uint32_t)pk, (uint32_t)(pk >> 32), kReach, 0x00020000u}, rv = {(uint32_t)pv, (uint32_t)(pv >> 32), kReach, 0x00020000u};
+    uint32_t saved;
+    static_assert(N == 2 || N == 3 || N == 4 || N == 8, "loads of a block");
+    if constexpr (N == 2)
+        asm volatile(RQ_BEGIN RQ_LOAD("a", "rk") RQ_NEXT RQ_LOAD("b", "rk") RQ_VALUES RQ_LOAD("e", "rv") RQ_NEXT RQ_LOAD("f", "rv") RQ_END
+                     : [saved] "=&s"(saved)
+                     : [a] "v"(k_from[0]), [b] "v"(k_from[1]), [e] "v"(v_from[0]), [f] "v"(v_from[1]), [rk] "s"(rk), [rv] "s"(rv),
+                       [at] "s"(at), [apart] "s"(apart)
+                     : "memory", "scc");
+    else if constexpr (N == 3)
+        asm volatile(RQ_BEGIN RQ_LOAD("a", "rk") RQ_NEXT RQ_LOAD("b", "rk") RQ_NEXT RQ_LOAD("c", "rk")
+                     RQ_VALUES RQ_LOAD("e", "rv") RQ_NEXT RQ_LOAD("f", "rv") RQ_NEXT RQ_LOAD("g", "rv") RQ_END
+                     : [saved] "=&s"(saved)
+                     : [a] "v"(k_from[0]), [b] "v"(k_from[1]), [c] "v"(k_from[2]), [e] "v"(v_from[0]), [f] "v"(v_from[1]), [g] "v"(v_from[2]),
+                       [rk] "s"(rk), [rv] "s"(rv), [at] "s"(at), [apart] "s"(apart)
+                     : "memory", "scc");
+    else {
+        asm volatile(RQ_BEGIN RQ_LOAD("a", "rk") RQ_NEXT RQ_LOAD("b", "rk") RQ_NEXT RQ_LOAD("c", "rk") RQ_NEXT RQ_LOAD("d", "rk")
+                     RQ_VALUES RQ_LOAD("e", "rv") RQ_NEXT RQ_LOAD("f", "rv") RQ_NEXT RQ_LOAD("g", "rv") RQ_NEXT RQ_LOAD("h", "rv") RQ_END
+                     : [saved] "=&s"(saved)
+                     : [a] "v"(k_from[0]), [b] "v"(k_from[1]), [c] "v"(k_from[2]), [d] "v"(k_from[3]), [e] "v"(v_from[0]), [f] "v"(v_from[1]),
+                       [g] "v"(v_from[2]), [h] "v"(v_from[3]), [rk] "s"(rk), [rv] "s"(rv), [at] "s"(at), [apart] "s"(apart)
+                     : "memory", "scc");
+        if constexpr (N == 8)
+            asm volatile(RQ_BEGIN RQ_LOAD("a", "rk") RQ_NEXT RQ_LOAD("b", "rk") RQ_NEXT RQ_LOAD("c", "rk") RQ_NEXT RQ_LOAD("d", "rk")
+                         RQ_VALUES RQ_LOAD("e", "rv") RQ_NEXT RQ_LOAD("f", "rv") RQ_NEXT RQ_LOAD("g", "rv") RQ_NEXT RQ_LOAD("h", "rv") RQ_END
+                         : [saved] "=&s"(saved)
+                         : [a] "v"(k_from[N - 4]), [b] "v"(k_from[N - 3]), [c] "v"(k_from[N - 2]), [d] "v"(k_from[N - 1]), [e] "v"(v_from[N - 4]),
+                           [f] "v"(v_from[N - 3]), [g] "v"(v_from[N - 2]), [h] "v"(v_from[N - 1]), [rk] "s"(rk), [rv] "s"(rv),
+                           [at] "s"(at + 4096), [apart] "s"(apart)
+                         : "memory", "scc");
+    }
+}
+// One of these loads, by the lanes in `lanes` (all or none).
+__device__ __forceinline__ void one_to_lds(u4 base, uint32_t from, uint32_t at, uint64_t lanes) {
     uint32_t saved;
     asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %3\n\t"
-        "s_nop 0\n\t"
-        "buffer_load_dwordx4 %1, %2, 0 offen lds\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
-        : "v"(offset), "s"(r), "s"(at)
+        "s_mov_b32 %[saved], m0\n\ts_mov_b32 m0, %[at]\n\ts_mov_b64 exec, %[lanes]\n\t" RQ_LOAD("a", "base")
+        "s_mov_b64 exec, -1\n\ts_mov_b32 m0, %[saved]"
+        : [saved] "=&s"(saved)
+        : [a] "v"(from), [base] "s"(base), [at] "s"(at), [lanes] "s"(lanes)
         : "memory");
 }
+#undef RQ_LOAD
+#undef RQ_NEXT
+#undef RQ_BEGIN
+#undef RQ_VALUES
+#undef RQ_END
 
 constexpr int kOthers = 64;   // parts of a problem, at most
 
@@ -203,7 +250,11 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
         }
     const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
     const int page_mask = (1 << a.c.page_log) - 1;
-    auto bring = [&](int j0, uint64_t bits, int buf) {
+    constexpr bool SPREAD = WIDE && !I8;   // the loads leave between the products of the scores
+    u4 k_base{}, v_base{};
+    uint32_t later_at = 0;
+    uint64_t later = 0;
+    auto bring = [&](int j0, uint64_t bits, int buf, bool now) {
 #pragma unroll
         for (int b = 0; b < BW; ++b) {
             const int block = wave * BW + b, in_bits = block * 16 - own, j = j0 + block * 16;
@@ -219,19 +270,22 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
             }
             const uint32_t part = (uint32_t)(bits >> in_bits) & 0xffffu;
             const uint32_t at = __builtin_amdgcn_readfirstlane(lds_at + buf * C::stage + block * 16 * PC * 16);
-            if (part == 0xffffu) {
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    to_lds(kp, k_from[i], at + i * 1024);
-                    to_lds(vp, v_from[i], at + C::half + i * 1024);
-                }
-            } else {
+            if (SPREAD && !now && part == 0xffffu) {
+                const uint64_t pk = reinterpret_cast<uint64_t>(kp), pv = reinterpret_cast<uint64_t>(vp);
+                k_base = u4{(uint32_t)pk, (uint32_t)(pk >> 32), kReach, 0x00020000u};
+                v_base = u4{(uint32_t)pv, (uint32_t)(pv >> 32), kReach, 0x00020000u};
+                later_at = at;
+                later = ~0ull;
+            } else if (part == 0xffffu) to_lds<NI>(kp, vp, k_from, v_from, at, C::half);
+            else {
+                uint32_t k_some[NI], v_some[NI];
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
                     const bool in = (part >> ((i * 64 + lane) / PC) & 1) != 0;
-                    to_lds(kp, in ? k_from[i] : kNowhere, at + i * 1024);
-                    to_lds(vp, in ? v_from[i] : kNowhere, at + C::half + i * 1024);
+                    k_some[i] = in ? k_from[i] : kNowhere;
+                    v_some[i] = in ? v_from[i] : kNowhere;
                 }
+                to_lds<NI>(kp, vp, k_some, v_some, at, C::half);
             }
         }
     };
@@ -287,7 +341,7 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
         fetch(job.begin);
         bits_next = settle();
         if constexpr (I8) load(job.begin);
-        else bring(job.begin, bits_next, 0);
+        else bring(job.begin, bits_next, 0, true);
         fetch(job.begin + KT);
     }
 
@@ -374,9 +428,10 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
             __builtin_amdgcn_s_waitcnt(0xf70);
             if constexpr (WIDE) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
             else asm volatile("" ::: "memory");
+            later = 0;
             if (more) {
                 bits_next = settle();
-                bring(j0 + KT, bits_next, buf ^ 1);
+                bring(j0 + KT, bits_next, buf ^ 1, false);
                 fetch(j0 + 2 * KT);
             }
         }
@@ -400,6 +455,16 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
 #pragma unroll
                         for (int n = 0; n < QP; ++n) s[nb][tb] = mfma32(k[tb & 1][ks], q[nb][ks][n], s[nb][tb]);
                     if (tb + 1 < TB) read_k(tb + 1, ks);
+                    // the next step's loads, spread: at once, a workgroup's would fill the way to LDS
+                    // and its waves wait (32760 queries x 512 keys 140 -> 129 us, heads of 256 260 -> 223)
+                    if constexpr (SPREAD) {
+                        const int slot = tb * KS + ks;
+#pragma unroll
+                        for (int i = 0; i < 2 * NI; ++i)
+                            if (slot == i * (TB * KS) / (2 * NI))
+                                one_to_lds(i < NI ? k_base : v_base, i < NI ? k_from[i] : v_from[i - NI],
+                                           later_at + (i < NI ? i * 1024 : C::half + (i - NI) * 1024), later);
+                    }
                     // (at 96 the order costs registers that a third wave needs)
                     if (DP != 96) __builtin_amdgcn_sched_barrier(0);
                 }
