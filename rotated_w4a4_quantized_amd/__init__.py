@@ -12,7 +12,14 @@ and the attention between such layers:
     rq.paged_attention(...) # one new token per sequence over a paged cache
     rq.cache_evict(...)     # cut the cache to a budget by attention weight
 
-attention.py puts them together: one decode step of a block.
+between the blocks, and attention of many queries to the same keys:
+
+    rq.block_norm(...)      # gated residual with the norms before and after it
+    rq.cross_attention(...) # to an encoder's states, or a block's own tokens
+    rq.prefix_attention(...)# paged attention behind a prefix the batch shares
+
+attention.py puts them together: one decode step of a block, and the attention
+of a diffusion transformer's block.
 
 The C ABI is include/rq.h; librq.so is built in-tree by
 `python -m rotated_w4a4_quantized_amd.build`.  Importing the package does not

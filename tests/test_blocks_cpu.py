@@ -297,3 +297,93 @@ def test_plain_attention_against_torch():
     assert (d > 0).all() and (d < 1e-4).all() and (dl < 1e-4).all()
     out, lse, d, dl = A.attention(q, k[:0], v[:0], 1.0, "f32")
     assert (out == 0).all() and np.isneginf(lse).all()
+
+
+# ------------------------------------------------------------------ the blocks' own bookkeeping
+
+def _weights(*shapes):
+    rng = np.random.default_rng(0)
+    return [rng.standard_normal(s).astype(np.float32) for s in shapes]
+
+
+def test_decode_block_behind_a_prefix(monkeypatch):
+    from rotated_w4a4_quantized_amd import attention
+    calls = []
+    hidden, hq, hkv, D, B, page = 128, 4, 2, 32, 3, 16
+    Ws = _weights(((hq + 2 * hkv) * D, hidden), (hidden, hq * D))
+    blk = attention.DecodeAttention(*Ws, hq, hkv, D, B, max_len=50, page=page, device="cpu", prefix=40)
+    for name in ("rotate_quant", "w4a4_linear", "paged_attention", "cache_evict"):
+        monkeypatch.setattr(rq, name, lambda *a, _n=name, **k: calls.append((_n, a, k)))
+    monkeypatch.setattr(rq, "qk_norm_rope", lambda *a, **k: calls.append(("store", k["cache"], {n: k[n].tolist() for n in ("positions", "place")},
+                                                                          k["seq"].tolist() if k.get("seq") is not None else None)))
+    monkeypatch.setattr(rq, "prefix_attention", lambda *a, **k: calls.append(("prefix", a[3], k["max_len"], a[4].tolist())))
+    x = torch.zeros(B, hidden, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        blk.step(x)                                    # no prefix yet
+    for bad in (torch.zeros(39, hidden, dtype=torch.bfloat16), torch.zeros(41, hidden, dtype=torch.bfloat16)):
+        with pytest.raises(ValueError):
+            blk.set_prefix(bad)
+    assert not calls
+    for _ in range(2):                                 # anew
+        calls.clear()
+        blk.set_prefix(torch.zeros(40, hidden, dtype=torch.bfloat16))
+        stored = [c for c in calls if c[0] == "store"]
+        assert sum((c[2]["place"] for c in stored), []) == list(range(40)) and all(c[1] is blk.prefix_cache for c in stored)
+        assert all(c[2]["place"] == c[2]["positions"] and set(c[3]) == {0} for c in stored)
+        calls.clear()
+        for t in range(10):
+            blk.step(x)
+        stored = [c for c in calls if c[0] == "store"]
+        assert [c[2]["place"] for c in stored] == [[40 + t] * B for t in range(10)] and all(c[1] is blk.cache for c in stored)
+        assert [c for c in calls if c[0] == "prefix"] == [("prefix", 40, 41 + t, [41 + t] * B) for t in range(10)]
+        assert not [c for c in calls if c[0] in ("paged_attention", "cache_evict")]
+        with pytest.raises(ValueError):
+            blk.step(x)                                # past max_len
+    # two full pages are shared; the third, which the prefix ends in, has copies, and no page is in two tables' own parts
+    t = blk.cache.table
+    assert (t[:, :2] == blk.prefix_table[:2]).all() and blk.prefix_table.tolist() == [0, 1, 2]
+    own = t[:, 2:].flatten().tolist()
+    assert len(set(own)) == len(own) and not set(own) & {0, 1, 2} and max(own) < blk.cache.k.shape[0]
+    plain = attention.DecodeAttention(*Ws, hq, hkv, D, B, max_len=50, page=page, device="cpu")
+    with pytest.raises(ValueError):
+        plain.set_prefix(x)
+    for kw in (dict(prefix=50), dict(prefix=-1), dict(prefix=8, budget=20)):
+        with pytest.raises(ValueError):
+            attention.DecodeAttention(*Ws, hq, hkv, D, B, max_len=50, page=page, device="cpu", **kw)
+
+
+def test_diffusion_block_refusals(monkeypatch):
+    from rotated_w4a4_quantized_amd import attention
+    hidden, heads, D, batch, tokens, states, caption = 128, 2, 64, 2, 5, 7, 64
+    inner = heads * D
+    Ws = _weights((3 * inner, hidden), (hidden, inner), (inner, hidden), (2 * inner, caption), (hidden, inner))
+    calls = []
+    for name in ("rotate_quant", "w4a4_linear", "qk_norm_rope", "block_norm", "cross_attention"):
+        monkeypatch.setattr(rq, name, lambda *a, _n=name, **k: calls.append((_n, a, k)))
+    blk = attention.DiffusionAttention(*Ws, heads, D, batch, tokens, states, device="cpu")
+    bf16 = torch.bfloat16
+    x, mod = torch.zeros(batch * tokens, hidden, dtype=bf16), torch.zeros(batch, 5, hidden)
+    with pytest.raises(ValueError):
+        blk.step(x, mod)                               # no captions yet
+    for bad in (torch.zeros(batch, 8, caption), torch.zeros(1, 3, caption), torch.zeros(batch, 0, caption), torch.zeros(batch, caption),
+                torch.zeros(batch, caption, 3).transpose(1, 2)):
+        with pytest.raises(ValueError):
+            blk.set_caption(bad.to(bf16))
+    assert not calls
+    blk.set_caption(torch.zeros(batch, 3, caption, dtype=bf16), lens=torch.ones(batch, dtype=torch.int32))
+    assert blk.states.keys == 3 and blk.states.c.k_stride == 3 * 2 * inner
+    calls.clear()
+    for bad in ((x[:-1], mod), (x, mod[:1]), (x, mod[:, :4]), (x, mod[..., :64])):
+        with pytest.raises(ValueError):
+            blk.step(*bad)
+    assert not calls
+    s = object()
+    blk.step(x, mod, stream=s)
+    assert [c[0] for c in calls if c[0] != "rotate_quant"] == [
+        "block_norm", "w4a4_linear", "qk_norm_rope", "cross_attention", "w4a4_linear", "block_norm", "w4a4_linear",
+        "cross_attention", "w4a4_linear", "block_norm"]
+    assert all(c[2]["stream"] is s for c in calls)
+    for i in range(5):
+        with pytest.raises(ValueError):
+            attention.DiffusionAttention(*[np.zeros((w.shape[0] + 8, w.shape[1]), np.float32) if j == i else w for j, w in enumerate(Ws)],
+                                         heads, D, batch, tokens, states, device="cpu")
