@@ -193,12 +193,12 @@ def _t_ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
+def _stream(stream, index=None):
     if stream is None:
         import torch
         # (the address alone: torch.cuda.current_stream() builds a Stream object
-        # around it, which costs as much as a launch)
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        # around it, which costs as much as a launch; index: the current device, where known)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index))
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -803,6 +803,8 @@ class Norm:
         if weight is not None and bias is not None and weight.device != bias.device:
             raise ValueError(f"weight and bias are on {weight.device} and {bias.device}")
         self.width, self.weight, self.bias = width, weight, bias
+        held = bias if weight is None else weight
+        self.device_index = None if held is None else held.get_device()
         self.c = c_norm(NORMS[kind], eps, _vector(weight, width, torch.float32, "weight"),
                         _vector(bias, width, torch.float32, "bias"))
         self._ref = ctypes.byref(self.c)
@@ -841,7 +843,7 @@ class Modulation:
         self.c = c_modulation(rows, 0, width if ld is None else ld, (1 << 62) if per is None else per, ptr(index),
                               ptr(gate), ptr(shift), ptr(scale))
         self._ref = ctypes.byref(self.c)
-        self._any = held[0][1]
+        self.device_index = held[0][1].get_device()
 
 
 def block_norm(x, z=None, pre: Norm = None, y=None, post: Norm = None, h=None, mod: Modulation = None, alpha=1.0,
@@ -850,32 +852,32 @@ def block_norm(x, z=None, pre: Norm = None, y=None, post: Norm = None, h=None, m
     post(y) and z = pre(h) (1 + scale) + shift, for rows x, h [T][width] of one
     type and y, z of one (fp32 or bf16 each).  Leave out y (nothing is added), h
     or z (not written).  h may be x itself, and z may be y."""
-    T, K = int(x.shape[0]), x.shape[-1]
-    io = y if y is not None else z
     if x.dim() != 2:
         raise ValueError("x must be rows [T][width]")
+    T, K = x.shape
+    index = x.get_device()
     if h is not None and h.dtype is not x.dtype:
         raise TypeError("h must have x's type")
     if y is not None and z is not None and y.dtype is not z.dtype:
         raise TypeError("z must have y's type")
-    for name, n in (("post", post), ("pre", pre)):
-        if n is not None and n.width != K:
-            raise ValueError(f"{name} is a norm of {n.width} values, the rows have {K}")
-    if mod is not None:
-        if mod.width != K:
-            raise ValueError(f"the modulations have {mod.width} values, the rows {K}")
-        if mod.index is not None and mod.index.numel() != T:
-            raise ValueError(f"index must have {T} elements, got {mod.index.numel()}")
-    _on_device(x.get_device(), y, h, z, None if mod is None else mod._any,
-               None if post is None else post.weight, None if post is None else post.bias,
-               None if pre is None else pre.weight, None if pre is None else pre.bias)
-    rows = (lambda t, name: (None, 0) if t is None else _rows(t, T, K, name))
+    for n in (post, pre, mod):
+        if n is not None:
+            if n.width != K:
+                raise ValueError(f"the rows have {K} values, a norm or the modulations {n.width}")
+            if n.device_index is not None and n.device_index != index:
+                raise ValueError(f"a norm or the modulations are on device {n.device_index}, x on {index}")
+    if mod is not None and mod.index is not None and mod.index.numel() != T:
+        raise ValueError(f"index must have {T} elements, got {mod.index.numel()}")
+    _on_device(index, y, h, z)
     p_x, x_ld = _rows(x, T, K, "x")
-    (p_y, y_ld), (p_h, h_ld), (p_z, z_ld) = rows(y, "y"), rows(h, "h"), rows(z, "z")
-    _check(load().rq_block_norm(
+    p_y, y_ld = (None, 0) if y is None else _rows(y, T, K, "y")
+    p_h, h_ld = (None, 0) if h is None else _rows(h, T, K, "h")
+    p_z, z_ld = (None, 0) if z is None else _rows(z, T, K, "z")
+    io = y if y is not None else z
+    _check((_lib or load()).rq_block_norm(
         None if post is None else post._ref, None if pre is None else pre._ref, None if mod is None else mod._ref, K,
         p_x, _io_dtype(x), x_ld, p_y, RQ_BF16 if io is None else _io_dtype(io), y_ld, T, alpha, beta, p_h, h_ld, p_z,
-        z_ld, _stream(stream)))
+        z_ld, _stream(stream, index)))
 
 
 def _tokens(t, name):
@@ -949,13 +951,14 @@ def cross_attention(q, states: States, out, scale=None, q_lens=None, lse=None, w
     B, T, H, D = q.shape
     if B != states.batch or D != states.head_dim:
         raise ValueError(f"q has {B} sequences of heads of {D}, the states {states.batch} of {states.head_dim}")
-    _on_device(q.get_device(), out, states.k, q_lens, lse, workspace)
+    index = q.get_device()
+    _on_device(index, out, states.k, q_lens, lse, workspace)
     (p_q, q_ld, q_b), (p_o, o_ld, o_b) = _tokens(q, "q"), _tokens(out, "out")
     p_ws, ws_bytes = _workspace(workspace)
     _check(load().rq_cross_attention(
         states._ref, p_q, _io_dtype(q), q_ld, q_b, T, H, D ** -0.5 if scale is None else scale,
         _vector(q_lens, B, torch.int32, "q_lens"), p_o, o_ld, o_b, _vector(lse, B * T * H, torch.float32, "lse"),
-        p_ws, ws_bytes, _stream(stream)))
+        p_ws, ws_bytes, _stream(stream, index)))
 
 
 def prefix_attention_workspace_bytes(cache: KVCache, q_heads: int, prefix: int, max_len: int, dtype) -> int:
@@ -979,7 +982,8 @@ def prefix_attention(q, cache: KVCache, prefix_table, prefix, lens, out, scale=N
     width = q.shape[1] if q.dim() == 2 else q.shape[1] * q.shape[2]
     if width % D:
         raise ValueError(f"a row of q must be whole heads of {D}, got {width}")
-    _on_device(q.get_device(), cache.k, prefix_table, lens, out, mask, lse, workspace)
+    index = q.get_device()
+    _on_device(index, cache.k, prefix_table, lens, out, mask, lse, workspace)
     p_q, q_ld = _rows(q, B, width, "q")
     p_o, o_ld = _rows(out, B, width, "out")
     if max_len is None:
@@ -997,4 +1001,4 @@ def prefix_attention(q, cache: KVCache, prefix_table, prefix, lens, out, scale=N
     _check(load().rq_prefix_attention(
         cache._ref, None if prefix_table is None or prefix == 0 else prefix_table.data_ptr(), prefix, p_q, dt, q_ld,
         width // D, D ** -0.5 if scale is None else scale, _vector(lens, B, torch.int32, "lens"), max_len, p_m, m_ld,
-        p_o, o_ld, _vector(lse, B * (width // D), torch.float32, "lse"), p_ws, ws_bytes, _stream(stream)))
+        p_o, o_ld, _vector(lse, B * (width // D), torch.float32, "lse"), p_ws, ws_bytes, _stream(stream, index)))
