@@ -191,7 +191,7 @@ struct Shape {
     static constexpr int bias = waves * 64 * 4;           // behind the two buffers: what each wave leaves out
     // at the end: rows of results, or of the waves' parts
     static constexpr int OP = DP + 4;                     // floats from row to row
-    static constexpr int ends = waves * NB * 32 * (OP * 4 + (TW > 1 ? 8 : 0)) + (TW > 1 ? kOthers * 256 + 256 : 0);
+    static constexpr int ends = waves * NB * 32 * (OP * 4 + (TW > 1 ? 8 : 0)) + (TW > 1 ? kOthers * 128 + 256 + threads * 16 : 0);
     static constexpr size_t lds = 2 * stage + bias > ends ? 2 * stage + bias : ends;
 };
 
@@ -651,47 +651,63 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
                     f4{o[0][db][4 * i], o[0][db][4 * i + 1], o[0][db][4 * i + 2], o[0][db][4 * i + 3]};
         __syncthreads();
         const int rows = min(32, job.R - job.row0);
-        // Parts that another launch left for these rows join here: their maxima, sums
-        // and then factors lie behind the waves' own.
+        // Parts that another launch left for these rows join here.  A wave a row: lane
+        // i has the other part i and, below TW, a wave's own; all factors come first.
         const int others = job.others;
-        f2 *ot = reinterpret_cast<f2 *>(st + C::TW * 64);
-        float *fin = st + C::TW * 64 + kOthers * 64;    // [32][2]: maximum and sum of all
-        for (int x = threadIdx.x; x < rows * others; x += C::threads) {
-            const int i = x / rows, r = x - i * rows;
-            ot[i * 32 + r] = reinterpret_cast<const f2 *>(a.stat)[i * a.rows + job.part + job.row0 + r];
-        }
-        if (others) __syncthreads();
-        if ((int)threadIdx.x < rows) {
-            const int r = threadIdx.x;
-            float M = -INFINITY, L = 0.0f;
-#pragma unroll
-            for (int w = 0; w < C::TW; ++w) M = fmaxf(M, st[(w * 32 + r) * 2]);
-            for (int i = 0; i < others; ++i) M = fmaxf(M, ot[i * 32 + r][0]);
-            auto part_of = [&](float mw, float lw) {
-                const float f = mw == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mw - M);
-                if (mw != -INFINITY) L += lw * f;
-                return f;
-            };
-#pragma unroll
-            for (int w = 0; w < C::TW; ++w) st[(w * 32 + r) * 2] = part_of(st[(w * 32 + r) * 2], st[(w * 32 + r) * 2 + 1]);
-            for (int i = 0; i < others; ++i) {
-                const f2 x = ot[i * 32 + r];
-                ot[i * 32 + r] = f2{part_of(x[0], x[1]), 0.0f};
+        float *of = st + C::TW * 64, *fin = of + kOthers * 32;   // [kOthers][32]; [32][2]: maximum and sum of all
+        for (int r = wave; r < rows; r += C::waves) {
+            f2 other = {-INFINITY, 0.0f}, own = {-INFINITY, 0.0f};
+            if (lane < others) other = reinterpret_cast<const f2 *>(a.stat)[lane * a.rows + job.part + job.row0 + r];
+            if (lane < C::TW) own = *reinterpret_cast<const f2 *>(st + (lane * 32 + r) * 2);
+            const float M = wave_max(fmaxf(other[0], own[0]));
+            const float mo = other[0], mw = own[0];
+            const float fo = mo == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mo - M), fw = mw == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mw - M);
+            const float L = wave_sum((mo == -INFINITY ? 0.0f : other[1] * fo) + (mw == -INFINITY ? 0.0f : own[1] * fw));
+            if (lane < others) of[lane * 32 + r] = fo;
+            if (lane < C::TW) st[(lane * 32 + r) * 2] = fw;
+            if (lane == 0) {
+                fin[r * 2] = M;
+                fin[r * 2 + 1] = L;
             }
-            fin[r * 2] = M;
-            fin[r * 2 + 1] = L;
         }
         __syncthreads();
-        for (int x = threadIdx.x; x < rows * (DP / 4); x += C::threads) {
-            const int r = x / (DP / 4), d = (x - r * (DP / 4)) * 4;
+        // the other parts, by as many threads as the rows leave
+        const int quads = DP / 4, items = rows * quads;
+        if (others) {
+            const int groups = C::threads > items ? C::threads / items : 1, group = (int)threadIdx.x / items;
+            for (int x = group < groups ? (int)threadIdx.x - group * items : items; x < items; x += C::threads) {
+                const int r = x / quads, d = (x - r * quads) * 4;
+                if (d >= D) continue;
+                f4 sum = {0, 0, 0, 0};
+                const float *other = a.part + (job.part + job.row0 + r) * D + d;
+#pragma unroll 8
+                for (int i = group; i < others; i += groups) sum += *reinterpret_cast<const f4 *>(other + i * a.rows * D) * of[i * 32 + r];
+                // (the waves' own outputs of the row, scaled, make room for the groups')
+                if (group == 0) {
+#pragma unroll
+                    for (int w = 0; w < C::TW; ++w) sum += *reinterpret_cast<const f4 *>(so + (w * 32 + r) * C::OP + d) * st[(w * 32 + r) * 2];
+                }
+                if (groups > 1) *reinterpret_cast<f4 *>(fin + 64 + (group * items + x) * 4) = sum;
+                else *reinterpret_cast<f4 *>(so + r * C::OP + d) = sum;
+            }
+            __syncthreads();
+            if (groups > 1 && (int)threadIdx.x < items) {
+                const int r = threadIdx.x / quads, d = (threadIdx.x - r * quads) * 4;
+                f4 sum = {0, 0, 0, 0};
+                for (int g = 0; g < groups; ++g) sum += *reinterpret_cast<const f4 *>(fin + 64 + (g * items + threadIdx.x) * 4);
+                *reinterpret_cast<f4 *>(so + r * C::OP + d) = sum;
+            }
+            if (groups > 1) __syncthreads();
+        }
+        for (int x = threadIdx.x; x < items; x += C::threads) {
+            const int r = x / quads, d = (x - r * quads) * 4;
             if (d >= D) continue;
             const float M = fin[r * 2], L = fin[r * 2 + 1];
             f4 sum = {0, 0, 0, 0};
+            if (others) sum = *reinterpret_cast<const f4 *>(so + r * C::OP + d);
+            else
 #pragma unroll
-            for (int w = 0; w < C::TW; ++w) sum += *reinterpret_cast<const f4 *>(so + (w * 32 + r) * C::OP + d) * st[(w * 32 + r) * 2];
-            const float *other = a.part + (job.part + job.row0 + r) * D + d;
-#pragma unroll 8
-            for (int i = 0; i < others; ++i) sum += *reinterpret_cast<const f4 *>(other + i * a.rows * D) * ot[i * 32 + r][0];
+                for (int w = 0; w < C::TW; ++w) sum += *reinterpret_cast<const f4 *>(so + (w * 32 + r) * C::OP + d) * st[(w * 32 + r) * 2];
             if (d == 0) put_stat(job.row0 + r, M, L);
             if (parts) *reinterpret_cast<f4 *>(a.part + (job.part + job.row0 + r) * D + d) = sum;
             else store4<BF16>(a.out, place_of(job.row0 + r) + d, sum * (M == -INFINITY ? 0.0f : 1.0f / L));
@@ -873,13 +889,20 @@ void join(const Args &a, hipStream_t s) {
         hipLaunchKernelGGL((join_rows_kernel<BF16, PREFIX, kJoin>), dim3((unsigned)a.rows), dim3(kJoin), 0, s, a);
 }
 
-// The kernel's shape for a number of rows: many rows divide over the waves, few
-// leave the waves the tokens.
+// The kernel's shape: many rows divide over the waves, few leave the waves the
+// tokens.  There, four waves a workgroup (heads of 65 to 128: one workgroup a CU) where a
+// CU has no more than one step of them to do, two (two a CU, which overlap) beyond: 5
+// sequences behind 1999 int8 tokens 18.4 us with four, 23.6 with two; 64 behind 16384
+// 59.4 and 53.3; 256 of 500 keys 42.6 and 36.3; 1 x 32760 keys 49.3 and 45.7.
+enum Kind { NARROW2 = 2, NARROW4 = 4, WIDE = 0 };
 constexpr int kNarrow = 32;
-int narrow_waves(int DP) { return DP <= 128 ? 4 : 2; }
+Kind kind_of(int DP, int64_t R, int64_t problems, int64_t keys) {
+    if (R > kNarrow) return WIDE;
+    return DP == 64 || (DP <= 128 && problems * ((keys + 127) / 128) <= device_cus()) ? NARROW4 : NARROW2;
+}
 int padded(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
-int rows_of(int64_t R) { return R <= kNarrow ? 32 : 128; }
-int step_of(int DP, int64_t R) { return R <= kNarrow ? narrow_waves(DP) * 32 : 64; }
+int rows_of(Kind k) { return k == WIDE ? 128 : 32; }
+int step_of(Kind k) { return k == WIDE ? 64 : k * 32; }
 
 // Parts of a problem of `keys` where `jobs` workgroups take one each.
 int parts_of(int64_t jobs, int64_t keys, int step, int least) {
@@ -895,10 +918,15 @@ void by_dim(int DP, F f) {
     else if (DP == 128) f(std::integral_constant<int, 128>{});
     else f(std::integral_constant<int, 256>{});
 }
-template <int DP, bool B, Source S>
-using Narrow = Shape<DP, B, 1, 1, DP <= 128 ? 4 : 2, S>;
-template <int DP, bool B, Source S>
-using Wide = Shape<DP, B, 1, 4, 1, S>;
+template <int DP, bool B, Source S, int WAVES>
+using Narrow = Shape<DP, B, 1, 1, WAVES, S>;
+// calls f with the shape of a narrow kind (those that kind_of() gives)
+template <int DP, bool B, Source S, class F>
+void narrow(Kind k, F f) {
+    if constexpr (DP <= 128)
+        if (k == NARROW4) return f(Narrow<DP, B, S, 4>{});
+    if constexpr (DP > 64) f(Narrow<DP, B, S, 2>{});
+}
 
 template <class C>
 int go(void (*kern)(Args), int64_t grid, const Args &a, hipStream_t s) {
@@ -911,6 +939,7 @@ int go(void (*kern)(Args), int64_t grid, const Args &a, hipStream_t s) {
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 struct CrossPlan {
+    Kind kind;
     int DP, tiles, splits;
     int64_t rows, grid;
     size_t part, stat;
@@ -920,10 +949,11 @@ CrossPlan cross_plan(const rq_states *s, int64_t queries, int q_heads, bool bf16
     const int G = q_heads / s->heads;
     const int64_t R = queries * G;
     p.DP = padded(s->head_dim);
-    const int rows = rows_of(R);
+    p.kind = kind_of(p.DP, R, (int64_t)s->heads * s->batch, s->keys);
+    const int rows = rows_of(p.kind);
     p.tiles = (int)((R + rows - 1) / rows);
     const int64_t jobs = (int64_t)p.tiles * s->heads * s->batch;
-    p.splits = parts_of(jobs, s->keys, step_of(p.DP, R), 4);
+    p.splits = parts_of(jobs, s->keys, step_of(p.kind), 4);
     p.grid = jobs * p.splits;
     p.rows = R * s->heads * s->batch;
     if (p.splits > 1) {
@@ -934,6 +964,7 @@ CrossPlan cross_plan(const rq_states *s, int64_t queries, int q_heads, bool bf16
 }
 
 struct PrefixPlan {
+    Kind kind, own_kind;
     int DP, tiles, splits, own_splits;
     int64_t rows, grid, own_grid;
     size_t part, stat;
@@ -943,12 +974,14 @@ PrefixPlan prefix_plan(const rq_kv_cache *c, int q_heads, bool bf16, int64_t pre
     const int G = q_heads / c->heads;
     const int64_t R = (int64_t)c->batch * G;
     p.DP = padded(c->head_dim);
-    const int rows = rows_of(R);
+    p.kind = kind_of(p.DP, R, c->heads, prefix);
+    const int rows = rows_of(p.kind);
     p.tiles = (int)((R + rows - 1) / rows);
-    if (prefix > 0) p.splits = parts_of((int64_t)p.tiles * c->heads, prefix, step_of(p.DP, R), 1);
+    if (prefix > 0) p.splits = parts_of((int64_t)p.tiles * c->heads, prefix, step_of(p.kind), 1);
     p.grid = (int64_t)p.tiles * c->heads * p.splits;
     const int own_tiles = (G + 31) / 32;
-    p.own_splits = parts_of((int64_t)own_tiles * c->heads * c->batch, max_len - prefix, step_of(p.DP, 1), 4);
+    p.own_kind = kind_of(p.DP, 1, (int64_t)own_tiles * c->heads * c->batch, max_len - prefix);
+    p.own_splits = parts_of((int64_t)own_tiles * c->heads * c->batch, max_len - prefix, step_of(p.own_kind), 4);
     p.own_grid = (int64_t)own_tiles * c->heads * c->batch * p.own_splits;
     p.rows = R * c->heads;
     const int parts = p.splits + (p.own_splits > 1 ? p.own_splits : 0);
@@ -997,8 +1030,9 @@ int launch_cross_attention(const rq_states *st, const void *q, int bf16, int64_t
     auto run = [&](auto dp, auto b) {
         constexpr int DP = decltype(dp)::value;
         constexpr bool B = decltype(b)::value;
-        if (queries * a.G <= kNarrow) err = go<Narrow<DP, B, STATES>>(cross_kernel<Narrow<DP, B, STATES>>, p.grid, a, s);
-        else err = go<Wide<DP, B, STATES>>(cross_kernel<Wide<DP, B, STATES>>, p.grid, a, s);
+        using W = Shape<DP, B, 1, 4, 1, STATES>;
+        if (p.kind == WIDE) err = go<W>(cross_kernel<W>, p.grid, a, s);
+        else narrow<DP, B, STATES>(p.kind, [&](auto n) { err = go<decltype(n)>(cross_kernel<decltype(n)>, p.grid, a, s); });
     };
     by_dim(p.DP, [&](auto dp) { bf16 ? run(dp, std::true_type{}) : run(dp, std::false_type{}); });
     if (err != 0) return err;
@@ -1037,13 +1071,12 @@ int launch_prefix_attention(const rq_kv_cache *c, const int32_t *prefix_table, i
         constexpr int DP = decltype(dp)::value;
         constexpr bool B = decltype(b)::value;
         constexpr Source S = decltype(src)::value;
-        using N = Narrow<DP, B, S>;
-        using W = Wide<DP, B, S>;
+        using W = Shape<DP, B, 1, 4, 1, S>;
         if (p.grid > 0) {
-            if ((int64_t)a.batch * a.G <= kNarrow) err = go<N>(prefix_kernel<N>, p.grid, a, s);
-            else err = go<W>(prefix_kernel<W>, p.grid, a, s);
+            if (p.kind == WIDE) err = go<W>(prefix_kernel<W>, p.grid, a, s);
+            else narrow<DP, B, S>(p.kind, [&](auto n) { err = go<decltype(n)>(prefix_kernel<decltype(n)>, p.grid, a, s); });
         }
-        if (err == 0) err = go<N>(own_kernel<N>, p.own_grid, a, s);
+        if (err == 0) narrow<DP, B, S>(p.own_kind, [&](auto n) { err = go<decltype(n)>(own_kernel<decltype(n)>, p.own_grid, a, s); });
     };
     by_dim(p.DP, [&](auto dp) {
         auto typed = [&](auto b) {
