@@ -718,7 +718,7 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
 // waves of a SIMD, by the registers they need
 template <class C>
 constexpr int resident() {
-    if (C::SRC == PAGES_I8) return C::BF16 && C::DP <= 128 && C::TW == 1 ? 2 : 1;
+    if (C::SRC == PAGES_I8) return C::BF16 && C::DP <= 96 && C::TW == 1 ? 2 : 1;
     return C::BF16 && C::DP <= 128 ? (C::DP == 96 ? 3 : 2) : 1;
 }
 
@@ -904,11 +904,15 @@ int padded(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
 int rows_of(Kind k) { return k == WIDE ? 128 : 32; }
 int step_of(Kind k) { return k == WIDE ? 64 : k * 32; }
 
-// Parts of a problem of `keys` where `jobs` workgroups take one each.
-int parts_of(int64_t jobs, int64_t keys, int step, int least) {
-    const int64_t steps = (keys + step - 1) / step, most = 2 * device_cus();
-    if (jobs >= device_cus() || jobs < 1) return 1;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({steps / least, most / jobs, kOthers}));
+// Parts of a problem of `keys` where `jobs` workgroups take one each, of `least`
+// steps at the least: as many as make two workgroups a CU; fp32 calls with heads up to
+// 64, whose steps take three times as long, four, so that uneven ones even out (5 uneven
+// sequences of 333 x 1999 54 -> 45 us; heads of 128, one workgroup a CU, lose: 4 of 1000 x
+// 2000 80 -> 104; and bf16 pays more for the parts: 77 queries x 32760 56 -> 67).
+int parts_of(int64_t jobs, int64_t keys, int step, int least, bool twice) {
+    const int64_t steps = (keys + step - 1) / step, enough = (twice ? 2 : 1) * (int64_t)device_cus();
+    if (jobs >= enough || jobs < 1) return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({steps / least, 2 * enough / jobs, kOthers}));
 }
 
 template <class F>
@@ -953,7 +957,7 @@ CrossPlan cross_plan(const rq_states *s, int64_t queries, int q_heads, bool bf16
     const int rows = rows_of(p.kind);
     p.tiles = (int)((R + rows - 1) / rows);
     const int64_t jobs = (int64_t)p.tiles * s->heads * s->batch;
-    p.splits = parts_of(jobs, s->keys, step_of(p.kind), 4);
+    p.splits = parts_of(jobs, s->keys, step_of(p.kind), 4, !bf16 && p.DP == 64);
     p.grid = jobs * p.splits;
     p.rows = R * s->heads * s->batch;
     if (p.splits > 1) {
@@ -977,11 +981,11 @@ PrefixPlan prefix_plan(const rq_kv_cache *c, int q_heads, bool bf16, int64_t pre
     p.kind = kind_of(p.DP, R, c->heads, prefix);
     const int rows = rows_of(p.kind);
     p.tiles = (int)((R + rows - 1) / rows);
-    if (prefix > 0) p.splits = parts_of((int64_t)p.tiles * c->heads, prefix, step_of(p.kind), 1);
+    if (prefix > 0) p.splits = parts_of((int64_t)p.tiles * c->heads, prefix, step_of(p.kind), 1, !bf16 && p.DP == 64);
     p.grid = (int64_t)p.tiles * c->heads * p.splits;
     const int own_tiles = (G + 31) / 32;
     p.own_kind = kind_of(p.DP, 1, (int64_t)own_tiles * c->heads * c->batch, max_len - prefix);
-    p.own_splits = parts_of((int64_t)own_tiles * c->heads * c->batch, max_len - prefix, step_of(p.own_kind), 4);
+    p.own_splits = parts_of((int64_t)own_tiles * c->heads * c->batch, max_len - prefix, step_of(p.own_kind), 4, false);
     p.own_grid = (int64_t)own_tiles * c->heads * c->batch * p.own_splits;
     p.rows = R * c->heads;
     const int parts = p.splits + (p.own_splits > 1 ? p.own_splits : 0);
