@@ -57,7 +57,8 @@ struct Args {
     int64_t rows;                  // rows of all problems: batch * heads * queries * G
     int32_t batch, queries, keys, hq, G;
     int32_t tiles, splits;         // row tiles and parts of a problem
-    Over by_G, by_batch, by_tiles, by_splits;
+    int32_t longest_first;         // 1: by_share.d jobs of each sequence on an XCD, the longest sequence's first
+    Over by_G, by_batch, by_tiles, by_splits, by_share;
     int32_t prefix, own_splits;    // shared prefix
     float scale2, q_factor;        // |scale| * log2(e); the queries' sign (0 with scale 0)
 };
@@ -739,11 +740,29 @@ __device__ __forceinline__ uint32_t job_of_block() {
 template <class C>
 __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu(resident<C>()))) cross_kernel(Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    // Sequences innermost: their lengths differ, and each XCD gets some of all.  They
-    // take turns in being first, or those of one length would meet on the same CUs.
-    const int id = job_of_block(), id1 = a.by_batch.of(id), id2 = a.by_tiles.of(id1), h = a.by_splits.of(id2);
-    const int turn = id - id1 * a.batch + id1 % a.batch, b = turn < a.batch ? turn : turn - a.batch;
-    const int tile = id1 - id2 * a.tiles, split = id2 - h * a.splits;
+    int b, id2;       // sequence; tile, part and head
+    if (a.longest_first) {
+        // Each XCD takes its share of the tiles of every sequence, the longest sequence's
+        // first: the last workgroups to start are short (5 uneven sequences of 333 fp32
+        // queries 45 -> 40 us, 4 of 4096 queries, 300 keys at most, 42 -> 41).
+        const int x = blockIdx.x % 8, l = blockIdx.x / 8, rank = a.by_share.of(l), lane = threadIdx.x & 63;
+        const int length = lane < a.batch ? min(max(a.lens[lane], 0), a.keys) : -1;
+        int mine = 0;
+        for (int i = 0; i < a.batch; ++i) {
+            const int other = __builtin_amdgcn_readlane(length, i);
+            mine += other > length || (other == length && i < lane);
+        }
+        b = __builtin_ctzll(__ballot(mine == rank));   // (ranks below the batch occur once)
+        id2 = x * a.by_share.d + l - rank * a.by_share.d;
+    } else {
+        // Sequences innermost: their lengths differ, and each XCD gets some of all.  They
+        // take turns in being first, or those of one length would meet on the same CUs.
+        const int id = job_of_block();
+        id2 = a.by_batch.of(id);
+        const int turn = id - id2 * a.batch + id2 % a.batch;
+        b = turn < a.batch ? turn : turn - a.batch;
+    }
+    const int id3 = a.by_tiles.of(id2), tile = id2 - id3 * a.tiles, h = a.by_splits.of(id3), split = id3 - h * a.splits;
     Job job;
     job.others = 0, job.to_parts = a.splits > 1;
     job.h = h;
@@ -1024,6 +1043,10 @@ int launch_cross_attention(const rq_states *st, const void *q, int bf16, int64_t
     a.batch = st->batch, a.hq = q_heads, a.G = q_heads / st->heads;
     a.tiles = p.tiles, a.splits = p.splits, a.rows = p.rows;
     a.by_G = over(a.G), a.by_batch = over(a.batch), a.by_tiles = over(a.tiles), a.by_splits = over(a.splits);
+    // (ranking costs a few instructions a sequence; the share has to be the same for all XCDs)
+    const int64_t each = p.grid / st->batch;
+    a.longest_first = st->lens && st->batch > 1 && st->batch <= 16 && each % 8 == 0;
+    a.by_share = over(std::max<int64_t>(each / 8, 1));
     set_scale(a, scale);
     if (p.splits > 1) {
         a.part = static_cast<float *>(workspace);
