@@ -3,7 +3,8 @@
 //   h = alpha x + beta gate (.) post(y);   z = pre(h) (.) (1 + scale) + shift
 //
 // with post and pre an RMS norm, a layer norm or nothing.  x and y are read once,
-// h and z written once: HBM bounds it.
+// h and z written once: HBM bounds it (32760 x 1536, fp32 stream, 604 MB in 124 us: 4.9
+// TB/s, a copy's rate; 8192 x 1152 in bf16 75 MB in 18 us, of which 15 are the bytes').
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -74,7 +75,11 @@ __device__ __forceinline__ void store8(void *p, int64_t at, const float (&f)[8])
 
 // WAVES waves take a token; a lane holds CH pieces of 8 of its values in registers,
 // always the same channels, so that the modulations stay in registers while the
-// tokens walk by.  RB, IB: x and h, y and z are bf16 (else fp32).
+// tokens walk by (read again for each token they would be more bytes, from the caches,
+// than the rows).  The next token's rows are on their way meanwhile.  Two waves a SIMD:
+// with one, 8192 x 1152 took 25 us against 20, 32760 x 1536 132 against 130; three have
+// too few registers (63 and 307).  Rows of up to 2048 values take one wave and no
+// barrier.  RB, IB: x and h, y and z are bf16 (else fp32).
 template <bool RB, bool IB, int WAVES, int CH>
 __global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) __attribute__((amdgpu_waves_per_eu(2))) block_norm_kernel(Args a) {
     constexpr int GROUPS = WAVES == 1 ? 4 : 1;   // tokens of a workgroup at a time
@@ -246,6 +251,7 @@ int launch_block_norm(const rq_norm *post, const rq_norm *pre, const rq_modulati
     a.T = (int)T, a.K = width, a.alpha = alpha, a.beta = beta;
     hipStream_t s = static_cast<hipStream_t>(stream);
     auto go = [&](auto kern, int waves) {
+        // (runs of tokens for twice the waves that are resident, or a wave where there are fewer)
         const int64_t most = (int64_t)device_cus() * (waves == 1 ? 16 : waves == 4 ? 4 : 2);
         a.run = (int)((T + most - 1) / most);
         const int64_t groups = (T + a.run - 1) / a.run, per_block = waves == 1 ? 4 : 1;
