@@ -838,6 +838,7 @@ typedef struct rq_modulation {
  * fp32 throughout:
  *   h = alpha x + beta gate (.) post(y);   z = pre(h) (.) (1 + scale) + shift
  * h and z are rounded once each (z is computed from h before its rounding).
+ * Means of squares are fp32: with eps 0, rows below 2^-63 lose digits.
  * Arguments:
  *   post, pre  norms, each may be NULL (none).  post needs y, pre needs z.
  *   mod        modulations or NULL (gate 1, shift 0, scale 0)
@@ -895,7 +896,8 @@ typedef struct rq_states {
 
 /*
  * Bytes of device workspace rq_cross_attention takes for these arguments.  It
- * depends on the descriptor's sizes, the other arguments and the device.
+ * depends on the descriptor's sizes, the other arguments and the device, never on
+ * lengths or data, and is no larger for fewer keys.
  * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_DTYPE.
  */
 rq_status rq_cross_attention_workspace_bytes(const rq_states *states, int64_t queries, int32_t q_heads,
@@ -908,9 +910,9 @@ rq_status rq_cross_attention_workspace_bytes(const rq_states *states, int64_t qu
  * whose mask is not 0:
  *   s_j = scale * sum_d q[d] k_j[d];  lse = log sum_j exp(s_j)
  *   out[d] = sum_j exp(s_j - lse) v_j[d]
- * Where no token is left: out is 0 and lse -infinity.  Keys and values that are
- * left out may hold anything, NaN included.  A NaN among the scores of a row
- * makes its out and lse NaN.
+ * Where no token is left: out is 0 and lse -infinity (and so where all scores are
+ * -infinity).  Keys and values that are left out may hold anything, NaN included.
+ * A NaN among the scores of a row makes its out and lse NaN.
  * Arguments:
  *   states     keys and values; their batch is that of the queries
  *   q          device, token t of sequence b at b * q_stride + t * q_ld: q_heads *
@@ -935,7 +937,8 @@ rq_status rq_cross_attention(const rq_states *states, const void *q, int32_t dty
 
 /*
  * Bytes of device workspace rq_prefix_attention takes for these arguments.  It
- * depends on the cache's sizes, the other arguments and the device.
+ * depends on the cache's sizes, the other arguments and the device, never on
+ * lengths or data, and is no larger for a smaller max_len.
  * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_DTYPE.
  */
 rq_status rq_prefix_attention_workspace_bytes(const rq_kv_cache *cache, int32_t q_heads, int32_t dtype,

@@ -199,6 +199,29 @@ def test_prefix_attention_without_work_and_workspace():
     assert size(None, 8, BF16, 40, 100, ctypes.byref(n)) == NULL
 
 
+def test_workspaces_grow_with_the_keys():
+    """A workspace for the longest call holds every shorter one."""
+    n = ctypes.c_size_t(0)
+    lengths = [*range(0, 700, 13), 1000, 1023, 1024, 1025, 2000, 5000, 20000, 100000]
+    for D in (64, 72, 128, 256):
+        for dtype in (BF16, F32):
+            for batch, heads, queries in ((1, 1, 1), (3, 4, 1), (40, 8, 1), (1, 12, 77), (2, 4, 300)):
+                last = 0
+                for keys in lengths:
+                    assert rq.load().rq_cross_attention_workspace_bytes(ref(states(head_dim=D, heads=heads, batch=batch, keys=keys)), queries,
+                                                                        heads * 2, dtype, ctypes.byref(n)) == 0
+                    assert n.value >= last
+                    last = n.value
+            for batch, heads in ((1, 1), (5, 8), (64, 8)):
+                for prefix in (0, 40, 999):
+                    last = 0
+                    for more in lengths:
+                        c = cache(head_dim=D, heads=heads, batch=batch, table_ld=1 << 14)
+                        assert rq.load().rq_prefix_attention_workspace_bytes(ref(c), heads * 2, dtype, prefix, prefix + more, ctypes.byref(n)) == 0
+                        assert n.value >= last
+                        last = n.value
+
+
 # ------------------------------------------------------------------ the binding
 
 def test_binding_norm_and_modulation():
