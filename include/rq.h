@@ -912,7 +912,8 @@ rq_status rq_cross_attention_workspace_bytes(const rq_states *states, int64_t qu
  *   out[d] = sum_j exp(s_j - lse) v_j[d]
  * Where no token is left: out is 0 and lse -infinity (and so where all scores are
  * -infinity).  Keys and values that are left out may hold anything, NaN included.
- * A NaN among the scores of a row makes its out and lse NaN.
+ * A NaN among the scores of a row makes its out and lse NaN, and so does a NaN or
+ * an infinity among its queries where a token is left.
  * Arguments:
  *   states     keys and values; their batch is that of the queries
  *   q          device, token t of sequence b at b * q_stride + t * q_ld: q_heads *

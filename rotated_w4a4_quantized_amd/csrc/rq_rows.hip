@@ -420,8 +420,10 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
         v_at[db] = C::half + (v_row0 * PC + v_place<PC>(v_row0, db * 4 + (lane >> 3 & 2) + (lane >> 1 & 1))) * 16 + (lane & 1) * 8;
 
     int buf = 0;
+    uint64_t any = 0;
     for (int j0 = job.begin; j0 < job.end; j0 += KT, buf ^= 1) {
         const uint64_t bits = bits_next;
+        any |= bits;
         const bool more = j0 + KT < job.end;
         if constexpr (I8) {
             // (the next write to this buffer is two steps away, behind the next step's barrier)
@@ -612,6 +614,11 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
         // through every join: exp2(inf - inf) is NaN, other parts count 0 beside it.
         if (l[nb] != l[nb]) m[nb] = INFINITY;
     }
+    // (slots that do not count give NaN, too, to a row whose queries are not finite)
+    const bool none = any == 0;
+    if (none)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) m[nb] = -INFINITY, l[nb] = 0.0f;
     __syncthreads();   // (the last step's LDS is read no more)
     if constexpr (WIDE) {
         constexpr bool H = BF16;               // rows of out in bf16, parts in fp32
@@ -626,7 +633,7 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int at = (nb * 32 + col) * OP + db * 32 + i * 8 + hf * 4;
-                    const f4 x = f4{o[nb][db][4 * i], o[nb][db][4 * i + 1], o[nb][db][4 * i + 2], o[nb][db][4 * i + 3]} * f;
+                    const f4 x = none ? f4{0, 0, 0, 0} : f4{o[nb][db][4 * i], o[nb][db][4 * i + 1], o[nb][db][4 * i + 2], o[nb][db][4 * i + 3]} * f;
                     if (H && !parts) store4<true>(mine, at, x);
                     else store4<false>(mine, at, x);
                 }
@@ -661,7 +668,7 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 *reinterpret_cast<f4 *>(so + (wave * 32 + col) * C::OP + db * 32 + i * 8 + hf * 4) =
-                    f4{o[0][db][4 * i], o[0][db][4 * i + 1], o[0][db][4 * i + 2], o[0][db][4 * i + 3]};
+                    none ? f4{0, 0, 0, 0} : f4{o[0][db][4 * i], o[0][db][4 * i + 1], o[0][db][4 * i + 2], o[0][db][4 * i + 3]};
         __syncthreads();
         const int rows = min(32, job.R - job.row0);
         // Parts that another launch left for these rows join here.  A wave a row: lane

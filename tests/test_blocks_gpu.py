@@ -517,6 +517,28 @@ def test_prefix_attention_missing_pages_and_junk(B, kind):
     assert (out == 0).all() and (lse == -float("inf")).all()
 
 
+@pytest.mark.parametrize("Tq, S", [(3, 150), (70, 150), (3, 4100)])
+def test_cross_attention_queries_that_are_not_finite(Tq, S):
+    """With no token left such a row is 0, too; else it is NaN, and its alone."""
+    hq, hkv, D = 4, 2, 72
+    for dtype in (torch.bfloat16, torch.float32):
+        rng = np.random.default_rng(Tq + S)
+        mask = np.ones((2, S), bool)
+        mask[1] = False
+        q = torch.from_numpy(rng.standard_normal((2, Tq, hq, D)).astype(np.float32)).cuda().to(dtype)
+        kv = torch.from_numpy(rng.standard_normal((2, S, 2, hkv, D)).astype(np.float32)).cuda().to(torch.bfloat16)
+        want, wl = run_cross(q, kv[:, :, 0], kv[:, :, 1], None, torch.from_numpy(mask).cuda(), None, None)
+        odd = q.clone()
+        odd[:, 1, 2, 5] = float("nan")
+        odd[:, 2, 1, 70] = float("inf")
+        got, gl = run_cross(odd, kv[:, :, 0], kv[:, :, 1], None, torch.from_numpy(mask).cuda(), None, None)
+        assert (got[1] == 0).all() and (gl[1] == -float("inf")).all()
+        for t, h in ((1, 2), (2, 1)):
+            assert got[0, t, h].isnan().all() and gl[0, t, h].isnan()
+            got[0, t, h], gl[0, t, h] = want[0, t, h], wl[0, t, h]
+        assert torch.equal(got, want) and torch.equal(gl, wl)
+
+
 def test_prefix_attention_equals_paged_attention_on_shared_pages():
     rng = np.random.default_rng(22)
     B, P, L, hq, hkv, D, page = 20, 192, 100, 8, 2, 128, 32
