@@ -912,8 +912,10 @@ rq_status rq_cross_attention_workspace_bytes(const rq_states *states, int64_t qu
  *   out[d] = sum_j exp(s_j - lse) v_j[d]
  * Where no token is left: out is 0 and lse -infinity (and so where all scores are
  * -infinity).  Keys and values that are left out may hold anything, NaN included.
- * A NaN among the scores of a row makes its out and lse NaN, and so does a NaN or
- * an infinity among its queries where a token is left.
+ * A NaN or +infinity among the scores of a row makes its out and lse NaN, and so does
+ * a NaN or an infinity among its queries where a token is left, and for fp32 queries
+ * an infinity among its keys.  An infinity among the values makes its column of out
+ * infinite or NaN.
  * Arguments:
  *   states     keys and values; their batch is that of the queries
  *   q          device, token t of sequence b at b * q_stride + t * q_ld: q_heads *
@@ -928,7 +930,9 @@ rq_status rq_cross_attention_workspace_bytes(const rq_states *states, int64_t qu
  *   workspace  device scratch of rq_cross_attention_workspace_bytes(), 16-byte
  *              aligned
  *   Rows of q and out must start 16-byte aligned.
- * Sums and softmax statistics are fp32.  The same inputs give the same bits.
+ * Sums and softmax statistics are fp32; the weights enter the product with the values
+ * with 16 bits for bf16 results and 24 for fp32 ones, as rq_paged_attention's.  The
+ * same inputs give the same bits.
  * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_DTYPE, RQ_ERR_ALIGN, RQ_ERR_HIP.
  */
 rq_status rq_cross_attention(const rq_states *states, const void *q, int32_t dtype, int64_t q_ld,

@@ -219,13 +219,17 @@ struct Shape {
 // there is no barrier.
 //
 // Rounding: K, V and bf16 queries enter exactly, fp32 queries as three bf16 parts
-// (24 bits).  Weights enter as bf16 for bf16 outputs and as three bf16 parts for
-// fp32 ones; sums and statistics are fp32.
+// (24 bits).  Weights enter as two bf16 parts (16 bits) for bf16 outputs and as three
+// for fp32 ones; sums and statistics are fp32.  One part for bf16 outputs would be off by
+// as much as the output's own rounding (from 64 bits 0.0025 relative in all, with two
+// 0.0017, as the rounding alone); the second costs 33% where the products are the bound
+// (9216 x 9216 tokens, 12 heads of 128: 545 -> 727 us), 8 to 17% on a caption's keys and at
+// most 10% elsewhere.
 template <class C>
 __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char *lds) {
     constexpr int DP = C::DP, NB = C::NB, KT = C::KT, TB = C::TB, PC = C::PC;
     constexpr bool BF16 = C::BF16, I8 = C::SRC == PAGES_I8, PAGED = C::SRC != STATES, WIDE = C::TW == 1;
-    constexpr int QP = BF16 ? 1 : 3;                  // parts of queries and weights
+    constexpr int QP = BF16 ? 1 : 3, WP = BF16 ? 2 : 3;   // parts of queries, of weights
     constexpr int KS = DP / 16, DB = DP / 32;
     constexpr int BW = KT / 16 / C::waves;            // blocks of 16 tokens a wave brings in
     constexpr int NI = PC / 4;                        // its loads a block, of K and of V
@@ -547,7 +551,7 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) base[nb] = m[nb] == -INFINITY ? 0.0f : -m[nb];
         constexpr int VB = DB < 8 ? 2 : 1;   // (with 8 products a group, the next group's values take the places of those used)
-        u4 v[VB][DB], p[2][NB][QP];
+        u4 v[VB][DB], p[2][NB][WP];
         auto read_v = [&](int g, int db) {
             const char *at = here + v_at[db] + g * 16 * PC * 16;
             const u2 x = read_turned(at), y = read_turned(at + 8 * PC * 16);
@@ -564,10 +568,10 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
                     const f2 x = *reinterpret_cast<const f2 *>(scales + KT + tb * 32 + (e / 4) * 8 + e % 4);
                     w0 *= x[0], w1 *= x[1];
                 }
-                uint32_t x[QP];
-                split2<QP>(w0, w1, x);
+                uint32_t x[WP];
+                split2<WP>(w0, w1, x);
 #pragma unroll
-                for (int n = 0; n < QP; ++n) p[g & 1][nb][n][i] = x[n];
+                for (int n = 0; n < WP; ++n) p[g & 1][nb][n][i] = x[n];
             }
         };
 #pragma unroll
@@ -583,7 +587,7 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int n = 0; n < QP; ++n) o[nb][db] = mfma32(v[g % VB][db], p[g & 1][nb][n], o[nb][db]);
+                    for (int n = 0; n < WP; ++n) o[nb][db] = mfma32(v[g % VB][db], p[g & 1][nb][n], o[nb][db]);
                 if (g + 1 < GROUPS) {
                     read_v(g + 1, db);
 #pragma unroll

@@ -1,0 +1,38 @@
+"""Attention to shared keys without a GPU: that the GPU tests' cases reach every
+kernel that a call can (by the rules of choice written out in tests/_rows.py, which
+the library's workspace sizes confirm)."""
+import ctypes
+
+import pytest
+
+from rotated_w4a4_quantized_amd import rq
+from tests import _rows as R
+from tests import test_blocks_gpu, test_rows_gpu
+from tests.test_blocks_cpu import BF16, F32, cache, ref, states
+
+torch = pytest.importorskip("torch")
+
+
+def test_the_cases_reach_every_kernel():
+    names = set()
+    for c in test_blocks_gpu.CROSS + test_rows_gpu.CROSS:
+        names |= R.cross(*c[:7], lens=c[7])[0]
+    for c in test_blocks_gpu.PREFIX + test_rows_gpu.PREFIX:
+        names |= R.prefix(*c[:8])[0]
+    assert names == R.every()
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the rules are written out for 256 CUs, which the library assumes without a GPU")
+def test_the_rules_are_the_library_s():
+    n = ctypes.c_size_t(0)
+    for c in test_blocks_gpu.CROSS + test_rows_gpu.CROSS:
+        B, Tq, S, hq, hkv, D, dtype = c[:7]
+        st = states(batch=B, keys=S, heads=hkv, head_dim=D)
+        assert rq.load().rq_cross_attention_workspace_bytes(ref(st), Tq, hq, BF16 if dtype == "bf16" else F32, ctypes.byref(n)) == 0
+        assert n.value == R.cross(*c[:7], lens=c[7])[1], c
+    for c in test_blocks_gpu.PREFIX + test_rows_gpu.PREFIX:
+        B, P, L, hq, hkv, D, dtype, kind, page = c[:9]
+        ch = cache(batch=B, heads=hkv, head_dim=D, page=page, table_ld=-(-(P + L) // page), dtype=BF16 if kind == "bf16" else rq.RQ_I8,
+                   k_scale=1 << 20, v_scale=1 << 20)
+        assert rq.load().rq_prefix_attention_workspace_bytes(ref(ch), hq, BF16 if dtype == "bf16" else F32, P, P + L, ctypes.byref(n)) == 0
+        assert n.value == R.prefix(*c[:8])[1], c
