@@ -68,6 +68,7 @@ struct Args {
     int64_t rows;                  // rows of all problems: batch * heads * queries * G
     int32_t batch, queries, keys, hq, G;
     int32_t tiles, splits;         // row tiles and parts of a problem
+    int32_t jobs;                  // of this launch
     int32_t longest_first;         // 1: by_share.d jobs of each sequence on an XCD, the longest sequence's first
     Over by_G, by_batch, by_tiles, by_splits, by_share, by_queries, by_heads, by_quads;
     int32_t prefix, own_splits;    // shared prefix
@@ -753,10 +754,14 @@ __device__ __forceinline__ void share(int begin, int end, int splits, int split,
     e = min(b + per, end);
 }
 
+// The workgroup's number (a launch holds 2^32 threads along x, so that many
+// workgroups go on along y; the last are more than there are jobs).
+__device__ __forceinline__ int block_of_launch() { return (int)(blockIdx.y * gridDim.x + blockIdx.x); }
+
 // Workgroups go round the 8 XCDs in turn; consecutive jobs, which share keys, are
 // given to the same one.
-__device__ __forceinline__ uint32_t job_of_block() {
-    const uint32_t n = gridDim.x, id = blockIdx.x, each = n / 8, more = n % 8, x = id % 8;
+__device__ __forceinline__ uint32_t job_of_block(uint32_t id, uint32_t n) {
+    const uint32_t each = n / 8, more = n % 8, x = id % 8;
     return x * each + min(x, more) + id / 8;
 }
 
@@ -764,11 +769,13 @@ template <class C>
 __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu(resident<C>()))) cross_kernel(Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     int b, id2;       // sequence; tile, part and head
+    const int block = block_of_launch();
+    if (block >= a.jobs) return;
     if (a.longest_first) {
         // Each XCD takes its share of the tiles of every sequence, the longest sequence's
         // first: the last workgroups to start are short (5 uneven sequences of 333 fp32
         // queries 45 -> 40 us, 4 of 4096 queries, 300 keys at most, 42 -> 41).
-        const int x = blockIdx.x % 8, l = blockIdx.x / 8, rank = a.by_share.of(l), lane = threadIdx.x & 63;
+        const int x = (uint32_t)block % 8, l = (uint32_t)block / 8, rank = a.by_share.of(l), lane = threadIdx.x & 63;
         const int length = lane < a.batch ? min(max(a.lens[lane], 0), a.keys) : -1;
         int mine = 0;
         for (int i = 0; i < a.batch; ++i) {
@@ -780,7 +787,7 @@ __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu
     } else {
         // Sequences innermost: their lengths differ, and each XCD gets some of all.  They
         // take turns in being first, or those of one length would meet on the same CUs.
-        const int id = job_of_block();
+        const int id = job_of_block(block, a.jobs);
         id2 = a.by_batch.of(id);
         const int turn = id - id2 * a.batch + id2 % a.batch;
         b = turn < a.batch ? turn : turn - a.batch;
@@ -813,7 +820,9 @@ __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu
 template <class C>
 __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu(resident<C>()))) prefix_kernel(Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    const int id = job_of_block(), id2 = a.by_tiles.of(id), tile = id - id2 * a.tiles;
+    const int block = block_of_launch();
+    if (block >= a.jobs) return;
+    const int id = job_of_block(block, a.jobs), id2 = a.by_tiles.of(id), tile = id - id2 * a.tiles;
     Job job;
     job.h = a.by_splits.of(id2);
     job.others = 0, job.to_parts = true;
@@ -833,7 +842,8 @@ template <class C>
 __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu(resident<C>()))) own_kernel(Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     const int tiles = (a.G + C::rows - 1) / C::rows;
-    uint32_t id = blockIdx.x;
+    uint32_t id = block_of_launch();
+    if ((int)id >= a.jobs) return;
     const int tile = id % tiles;
     id /= tiles;
     const int split = id % max(a.own_splits, 1);
@@ -1020,10 +1030,13 @@ void narrow(Kind k, F f) {
 }
 
 template <class C>
-int go(void (*kern)(Args), int64_t grid, const Args &a, hipStream_t s) {
+int go(void (*kern)(Args), int64_t jobs, Args &a, hipStream_t s) {
+    constexpr int64_t most = 1 << 23;   // workgroups along x
+    a.jobs = (int)jobs;
+    const dim3 grid((unsigned)std::min(jobs, most), (unsigned)((jobs + most - 1) / most));
     const int err = ensure_dyn_lds(reinterpret_cast<const void *>(kern), C::lds);
     if (err != (int)hipSuccess) return err;
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(C::threads), C::lds, s, a);
+    hipLaunchKernelGGL(kern, grid, dim3(C::threads), C::lds, s, a);
     return (int)hipSuccess;
 }
 
@@ -1089,9 +1102,7 @@ void set_scale(Args &a, float scale) {
 }  // namespace
 
 bool cross_fits(const rq_states *s, int64_t queries, int q_heads, int bf16) {
-    const CrossPlan p = cross_plan(s, queries, q_heads, bf16);
-    // (a launch holds 2^32 threads)
-    return p.grid < (1 << 24) && p.rows < (int64_t(1) << 25);
+    return cross_plan(s, queries, q_heads, bf16).rows < (int64_t(1) << 25);
 }
 size_t cross_workspace_bytes(const rq_states *s, int64_t queries, int q_heads, int bf16) {
     const CrossPlan p = cross_plan(s, queries, q_heads, bf16);
@@ -1137,8 +1148,7 @@ int launch_cross_attention(const rq_states *st, const void *q, int bf16, int64_t
 }
 
 bool prefix_fits(const rq_kv_cache *c, int q_heads, int bf16, int64_t prefix, int64_t max_len) {
-    const PrefixPlan p = prefix_plan(c, q_heads, bf16, prefix, max_len);
-    return p.grid < (1 << 24) && p.own_grid < (1 << 24) && p.rows < (int64_t(1) << 25);
+    return prefix_plan(c, q_heads, bf16, prefix, max_len).rows < (int64_t(1) << 25);
 }
 size_t prefix_workspace_bytes(const rq_kv_cache *c, int q_heads, int bf16, int64_t prefix, int64_t max_len) {
     const PrefixPlan p = prefix_plan(c, q_heads, bf16, prefix, max_len);

@@ -36,3 +36,18 @@ def test_the_rules_are_the_library_s():
                    k_scale=1 << 20, v_scale=1 << 20)
         assert rq.load().rq_prefix_attention_workspace_bytes(ref(ch), hq, BF16 if dtype == "bf16" else F32, P, P + L, ctypes.byref(n)) == 0
         assert n.value == R.prefix(*c[:8])[1], c
+
+
+@pytest.mark.parametrize("heads,G,fits", [(256, 1, True), (300, 1, True), (512, 1, True), (513, 1, False), (256, 2, True), (171, 3, False)])
+def test_the_limit_of_rows_is_the_stated_one(heads, G, fits):
+    """batch * queries * q_heads < 2^25, however many workgroups that takes."""
+    n = ctypes.c_size_t(0)
+    assert (65535 * heads * G < 1 << 25) == fits
+    want = 0 if fits else -2
+    st = states(batch=65535, heads=heads, head_dim=16, keys=3)
+    assert rq.load().rq_cross_attention_workspace_bytes(ref(st), 1, heads * G, BF16, ctypes.byref(n)) == want
+    for prefix, max_len in ((0, 16), (3, 16)):
+        c = cache(batch=65535, heads=heads, head_dim=16, table_ld=1, pages=1)
+        assert rq.load().rq_prefix_attention_workspace_bytes(ref(c), heads * G, BF16, prefix, max_len, ctypes.byref(n)) == want
+    if not fits:
+        assert b"2^25" in rq.load().rq_last_error()

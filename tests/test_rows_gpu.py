@@ -161,3 +161,31 @@ def test_prefix_attention_is_as_exact_as_paged_attention(B, L, dtype, kind):
     ws = torch.empty(max(16, rq.paged_attention_workspace_bytes(whole, hq, P + L)), dtype=torch.uint8, device="cuda")
     rq.paged_attention(q, whole, short, o2, max_len=P + L, lse=l2, workspace=ws)
     check_prefix(o2, l2, *plain)
+
+
+def test_more_workgroups_than_a_launch_holds_along_one_axis():
+    # 2^24 and more (one each for a sequence and head): the same bits as a part of the sequences at a time
+    B, H, D, page, each = 65535, 300, 16, 16, 16000
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.randn(B, 1, H, D, generator=g, device="cuda", dtype=torch.bfloat16)
+    kv = torch.randn(2, page, H, D, generator=g, device="cuda", dtype=torch.bfloat16)
+    lens = torch.randint(0, page + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    k, v = (kv[i, None].expand(B, page, H, D) for i in (0, 1))
+    out, lse = run_cross(q, k, v, lens, None, None, None)
+    pages = kv.transpose(1, 2)[:, None].contiguous()
+    table = torch.zeros(B, 1, dtype=torch.int32, device="cuda")
+    o2, l2 = run_prefix(q.view(B, -1), rq.KVCache(pages[0], pages[1], table), None, 0, lens, page, H)
+    for b in range(0, B, each):
+        s = slice(b, min(b + each, B))
+        part, part_lse = run_cross(q[s], k[s], v[s], lens[s].contiguous(), None, None, None)
+        assert same_bits(part, out[s]) and same_bits(part_lse, lse[s])
+        part, part_lse = run_prefix(q[s].view(-1, H * D), rq.KVCache(pages[0], pages[1], table[s]), None, 0, lens[s].contiguous(), page, H)
+        assert same_bits(part, o2[s]) and same_bits(part_lse, l2[s])
+    kn, vn = (num(t) for t in kv)
+    for b in (0, 1, each - 1, 40000, B - 1):
+        n = int(lens[b])
+        for h in (0, 7, H - 1):
+            o, l, do, dl = R.attention(num(q[b, :, h]), kn[:n, h], vn[:n, h], D ** -0.5, "bf16")
+            for got, gl in ((out[b, :, h], lse[b, :, h]), (o2[b].view(H, D)[h:h + 1], l2[b, h:h + 1])):
+                within(num(got), o, do, "out")
+                within(num(gl), l, dl, "lse")
