@@ -913,8 +913,8 @@ rq_status rq_cross_attention_workspace_bytes(const rq_states *states, int64_t qu
  * Where no token is left: out is 0 and lse -infinity (and so where all scores are
  * -infinity).  Keys and values that are left out may hold anything, NaN included.
  * A NaN or +infinity among the scores of a row makes its out and lse NaN, and so does
- * a NaN or an infinity among its queries where a token is left, and for fp32 queries
- * an infinity among its keys.  An infinity among the values makes its column of out
+ * a NaN or an infinity among its queries where a token is left.  With fp32 queries an
+ * infinity among the keys may, too; one among the values makes its column of out
  * infinite or NaN.
  * Arguments:
  *   states     keys and values; their batch is that of the queries

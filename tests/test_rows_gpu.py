@@ -189,3 +189,36 @@ def test_more_workgroups_than_a_launch_holds_along_one_axis():
             for got, gl in ((out[b, :, h], lse[b, :, h]), (o2[b].view(H, D)[h:h + 1], l2[b, h:h + 1])):
                 within(num(got), o, do, "out")
                 within(num(gl), l, dl, "lse")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("Tq,S", [(2, 150), (60, 150), (2, 2000)])
+def test_cross_attention_to_infinities(Tq, S, dtype):
+    """What a score of +-infinity and an infinite value lead to."""
+    rng = np.random.default_rng(S)
+    H, D = 2, 64
+    q, qn = rand(rng, (1, Tq, H, D), dtype)
+    kv, kvn = rand(rng, (1, S, 2, H, D), "bf16")
+    j = S // 3
+    # a key of infinity in one coordinate: +-infinity times the query's, of either sign
+    q[..., 3], qn[..., 3] = 1.5, 1.5
+    q[0, 1, :, 3], qn[0, 1, :, 3] = -1.5, -1.5
+    inf = kv.clone()
+    inf[0, j, 0, :, 3] = float("inf")
+    out, lse = run_cross(q, inf[:, :, 0], inf[:, :, 1], None, None, None, None)
+    assert out[0, 0].isnan().all() and lse[0, 0].isnan().all()              # a score of +infinity
+    if dtype == "bf16":                                                     # a score of -infinity: the token does not count
+        at = np.delete(np.arange(S), j)
+        for h in range(H):
+            o, l, do, dl = R.attention(qn[0, 1:2, h].astype(np.float64), kvn[0, at, 0, h].astype(np.float64),
+                                       kvn[0, at, 1, h].astype(np.float64), D ** -0.5, dtype)
+            within(num(out[0, 1:2, h]), o, do, "out")
+            within(num(lse[0, 1:2, h]), l, dl, "lse")
+    # an infinite value: its column alone
+    inf = kv.clone()
+    inf[0, j, 1, 0, 5] = float("inf")
+    want, wl = run_cross(q, kv[:, :, 0], kv[:, :, 1], None, None, None, None)
+    out, lse = run_cross(q, inf[:, :, 0], inf[:, :, 1], None, None, None, None)
+    assert not out[0, :, 0, 5].isfinite().any()
+    out[0, :, 0, 5] = want[0, :, 0, 5]
+    assert same_bits(out, want) and same_bits(lse, wl)
