@@ -922,7 +922,7 @@ rq_status rq_cross_attention_workspace_bytes(const rq_states *states, int64_t qu
  *              D values of dtype (RQ_F32 or RQ_BF16)
  *   queries    tokens of a sequence, 0 .. 2^24; batch * queries * q_heads < 2^25
  *   q_heads    a multiple of the states' heads, at most 1024
- *   scale      multiplies the scores (finite)
+ *   scale      multiplies the scores (at most 2^127 in magnitude)
  *   q_lens     device int32 [batch] or NULL: tokens from q_lens[b] on are not
  *              computed and their rows of out and lse not written
  *   out        device, as q; must not alias q
@@ -959,6 +959,7 @@ rq_status rq_prefix_attention_workspace_bytes(const rq_kv_cache *cache, int32_t 
  * table.  A sequence with lens[b] < prefix or lens[b] < 1 has no token in the
  * batch: its out is 0 and its lse -infinity.
  * Arguments as rq_paged_attention, and
+ *   scale      at most 2^127 in magnitude
  *   prefix_table  device int32 [ceil(prefix / page)], 16-byte aligned (NULL when
  *              prefix is 0).  An entry outside [0, pages): no page there.
  *   prefix     0 <= prefix <= max_len

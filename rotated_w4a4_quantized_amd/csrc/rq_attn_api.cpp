@@ -121,6 +121,12 @@ rq_status check_prefix(const rq_kv_cache *c, int q_heads, int dtype, int64_t pre
     return RQ_OK;
 }
 
+// (the kernels multiply by scale log2(e), which has to be finite, too)
+rq_status check_scale(float scale) {
+    if (!(std::fabs(scale) <= 0x1p127f)) return fail(RQ_ERR_SHAPE, "scale must be finite, at most 2^127 in magnitude");
+    return RQ_OK;
+}
+
 rq_status check_workspace(const char *what, size_t need, const void *workspace, size_t have) {
     if (need == 0) return RQ_OK;
     if (!workspace || have < need)
@@ -313,7 +319,7 @@ rq_status rq_cross_attention(const rq_states *states, const void *q, int32_t dty
     clear_error();
     rq_status st = check_cross(states, queries, q_heads, dtype);
     if (st != RQ_OK) return st;
-    if (!std::isfinite(scale)) return fail(RQ_ERR_SHAPE, "scale must be finite");
+    if ((st = check_scale(scale)) != RQ_OK) return st;
     const int D = states->head_dim;
     const int64_t row = (int64_t)q_heads * D, kv = (int64_t)states->heads * D;
     // (rows of at most 2^31 elements and sequences of 2^46 keep every offset below 2^63)
@@ -370,7 +376,7 @@ rq_status rq_prefix_attention(const rq_kv_cache *cache, const int32_t *prefix_ta
     clear_error();
     rq_status st = check_prefix(cache, q_heads, dtype, prefix, max_len, true);
     if (st != RQ_OK) return st;
-    if (!std::isfinite(scale)) return fail(RQ_ERR_SHAPE, "scale must be finite");
+    if ((st = check_scale(scale)) != RQ_OK) return st;
     const int64_t row = (int64_t)q_heads * cache->head_dim, wide = int64_t(1) << 31;
     if (q_ld < row || q_ld > wide || out_ld < row || out_ld > wide)
         return fail(RQ_ERR_SHAPE, "q_ld and out_ld must hold a row of q_heads * head_dim");

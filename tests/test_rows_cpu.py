@@ -8,7 +8,7 @@ import pytest
 from rotated_w4a4_quantized_amd import rq
 from tests import _rows as R
 from tests import test_blocks_gpu, test_rows_gpu
-from tests.test_blocks_cpu import BF16, F32, cache, ref, states
+from tests.test_blocks_cpu import BF16, F32, SHAPE, cache, call_cross, call_prefix, ref, states
 
 torch = pytest.importorskip("torch")
 
@@ -43,7 +43,7 @@ def test_the_limit_of_rows_is_the_stated_one(heads, G, fits):
     """batch * queries * q_heads < 2^25, however many workgroups that takes."""
     n = ctypes.c_size_t(0)
     assert (65535 * heads * G < 1 << 25) == fits
-    want = 0 if fits else -2
+    want = 0 if fits else SHAPE
     st = states(batch=65535, heads=heads, head_dim=16, keys=3)
     assert rq.load().rq_cross_attention_workspace_bytes(ref(st), 1, heads * G, BF16, ctypes.byref(n)) == want
     for prefix, max_len in ((0, 16), (3, 16)):
@@ -51,3 +51,11 @@ def test_the_limit_of_rows_is_the_stated_one(heads, G, fits):
         assert rq.load().rq_prefix_attention_workspace_bytes(ref(c), heads * G, BF16, prefix, max_len, ctypes.byref(n)) == want
     if not fits:
         assert b"2^25" in rq.load().rq_last_error()
+
+
+@pytest.mark.parametrize("scale", [3e38, -2.0 ** 127 * 1.001, float("inf"), float("nan")])
+def test_scales_that_overflow_are_refused(scale):
+    """scale log2(e) has to be finite, too, or a score of 0 would be 0 times infinity."""
+    assert call_cross(scale=scale) == SHAPE
+    assert call_prefix(scale=scale) == SHAPE
+    assert call_cross(states(batch=0), scale=2.0 ** 127) == 0 and call_prefix(cache(batch=0), scale=-2.0 ** 127) == 0
