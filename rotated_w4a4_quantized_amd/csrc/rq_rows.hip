@@ -187,14 +187,14 @@ __device__ __forceinline__ void one_to_lds(u4 base, uint32_t from, uint32_t at, 
 
 constexpr int kOthers = 64;   // parts of a problem, at most
 
-// NB blocks of 32 rows a wave; RW waves along the rows, or TW along the tokens.
-template <int DP_, bool BF16_, int NB_, int RW_, int TW_, Source SRC_>
+// 32 rows a wave; RW waves along the rows, or TW along the tokens.
+template <int DP_, bool BF16_, int RW_, int TW_, Source SRC_>
 struct Shape {
-    static constexpr int DP = DP_, NB = NB_, RW = RW_, TW = TW_;
+    static constexpr int DP = DP_, RW = RW_, TW = TW_;
     static constexpr bool BF16 = BF16_;
     static constexpr Source SRC = SRC_;
     static constexpr int waves = RW * TW, threads = waves * 64;
-    static constexpr int rows = RW * NB * 32;
+    static constexpr int rows = RW * 32;
     static constexpr int TB = TW == 1 ? 2 : 1;            // blocks of 32 tokens a wave takes in a step
     static constexpr int KT = TW * TB * 32;               // tokens of a step
     static constexpr int PC = DP / 8;                     // pieces of a row
@@ -204,7 +204,7 @@ struct Shape {
     static constexpr int bias = waves * 64 * 4;           // behind the two buffers: what each wave leaves out
     // at the end: rows of results, or of the waves' parts
     static constexpr int OP = DP + 4;                     // floats from row to row
-    static constexpr int ends = waves * NB * 32 * (OP * 4 + (TW > 1 ? 8 : 0)) + (TW > 1 ? kOthers * 128 + 256 + threads * 16 : 0);
+    static constexpr int ends = waves * 32 * (OP * 4 + (TW > 1 ? 8 : 0)) + (TW > 1 ? kOthers * 128 + 256 + threads * 16 : 0);
     static constexpr size_t lds = 2 * stage + bias > ends ? 2 * stage + bias : ends;
 };
 
@@ -228,7 +228,7 @@ struct Shape {
 // most 10% elsewhere.
 template <class C>
 __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char *lds) {
-    constexpr int DP = C::DP, NB = C::NB, KT = C::KT, TB = C::TB, PC = C::PC;
+    constexpr int DP = C::DP, KT = C::KT, TB = C::TB, PC = C::PC;
     constexpr bool BF16 = C::BF16, I8 = C::SRC == PAGES_I8, PAGED = C::SRC != STATES, WIDE = C::TW == 1;
     constexpr int QP = BF16 ? 1 : 3, WP = BF16 ? 2 : 3;   // parts of queries, of weights
     constexpr int KS = DP / 16, DB = DP / 32;
@@ -363,56 +363,47 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
     }
 
     // ---- rows and queries
-    int row[NB];
-    u4 q[NB][KS][QP];
+    const int row = job.row0 + (WIDE ? wave * 32 : 0) + col;
+    const int r0 = min(row, job.R - 1), t0 = a.by_G.of(r0);
+    const int64_t q_at = job.q_at + t0 * a.q_ld + (int64_t)(job.h * G + r0 - t0 * G) * D;
+    u4 q[KS][QP];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        row[nb] = job.row0 + ((WIDE ? wave * NB : 0) + nb) * 32 + col;
-        const int r = min(row[nb], job.R - 1), t = a.by_G.of(r), g = r - t * G;
-        const int64_t at = job.q_at + t * a.q_ld + (int64_t)(job.h * G + g) * D;
+    for (int ks = 0; ks < KS; ++ks) {
+        // (past D: any of the row, K is zero there)
+        const int d = ks * 16 + hf * 8 < D ? ks * 16 + hf * 8 : 0;
+        if constexpr (BF16) {
+            q[ks][0] = *reinterpret_cast<const u4 *>(static_cast<const uint16_t *>(a.q) + q_at + d);
+        } else {
+            const float *p = static_cast<const float *>(a.q) + q_at + d;
+            const f4 x = *reinterpret_cast<const f4 *>(p), y = *reinterpret_cast<const f4 *>(p + 4);
+            const float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            // (past D: any of the row, K is zero there)
-            const int d = ks * 16 + hf * 8 < D ? ks * 16 + hf * 8 : 0;
-            if constexpr (BF16) {
-                q[nb][ks][0] = *reinterpret_cast<const u4 *>(static_cast<const uint16_t *>(a.q) + at + d);
-            } else {
-                const float *p = static_cast<const float *>(a.q) + at + d;
-                const f4 x = *reinterpret_cast<const f4 *>(p), y = *reinterpret_cast<const f4 *>(p + 4);
-                const float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+            for (int i = 0; i < 4; ++i) {
+                uint32_t p3[3];
+                split2<3>(z[2 * i], z[2 * i + 1], p3);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t p3[3];
-                    split2<3>(z[2 * i], z[2 * i + 1], p3);
-#pragma unroll
-                    for (int n = 0; n < QP; ++n) q[nb][ks][n][i] = p3[n];
-                }
+                for (int n = 0; n < QP; ++n) q[ks][n][i] = p3[n];
             }
         }
-        if (a.q_factor != 1.0f) {
+    }
+    if (a.q_factor != 1.0f) {
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                for (int n = 0; n < QP; ++n)
+            for (int n = 0; n < QP; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t x = q[nb][ks][n][i];
-                        q[nb][ks][n][i] = pack2(lo_of(x) * a.q_factor, hi_of(x) * a.q_factor);
-                    }
-        }
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t x = q[ks][n][i];
+                    q[ks][n][i] = pack2(lo_of(x) * a.q_factor, hi_of(x) * a.q_factor);
+                }
     }
 
-    f16 o[NB][DB];
-    float m[NB], l[NB];
+    f16 o[DB];
+    float m = -INFINITY, l = 0.0f;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        m[nb] = -INFINITY;
-        l[nb] = 0.0f;
+    for (int db = 0; db < DB; ++db)
 #pragma unroll
-        for (int db = 0; db < DB; ++db)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[nb][db][i] = 0.0f;
-    }
+        for (int i = 0; i < 16; ++i) o[db][i] = 0.0f;
 
     // the lane's places in LDS, without the token block
     int k_at[KS], v_at[DB];
@@ -455,7 +446,7 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
             }
         }
         const char *here = lds + buf * C::stage;
-        f16 s[NB][TB];
+        f16 s[TB];
         // Reads leave a block of products ahead, into the places of what was just used (left
         // to itself, the compiler has each product wait for its own).
         auto scores = [&](auto from) {
@@ -470,9 +461,7 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int n = 0; n < QP; ++n) s[nb][tb] = mfma32(k[ks], q[nb][ks][n], s[nb][tb]);
+                    for (int n = 0; n < QP; ++n) s[tb] = mfma32(k[ks], q[ks][n], s[tb]);
                     if (tb + 1 < TB) read_k(tb + 1, ks);
                     // the next step's loads, spread: at once, a workgroup's would fill the way to LDS
                     // and its waves wait (32760 queries x 512 keys 140 -> 129 us, heads of 256 260 -> 223)
@@ -492,9 +481,7 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
         if (bits == (WIDE ? ~0ull : 0xffffffffull)) {
             scores([&](int tb) {
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) s[nb][tb][i] = 0.0f;
+                for (int i = 0; i < 16; ++i) s[tb][i] = 0.0f;
             });
         } else {
             // slots that do not count start from -infinity (their keys are zeros)
@@ -505,9 +492,7 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
                 for (int i = 0; i < 16; i += 4) {
                     const f4 x = *reinterpret_cast<const f4 *>(bias + tb * 32 + i * 2 + hf * 4);
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[nb][tb][i + e] = x[e];
+                    for (int e = 0; e < 4; ++e) s[tb][i + e] = x[e];
                 }
             });
         }
@@ -520,39 +505,32 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
                 for (int i = 0; i < 16; i += 4) {
                     const f4 x = *reinterpret_cast<const f4 *>(scales + tb * 32 + i * 2);
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[nb][tb][i + e] *= x[e];
+                    for (int e = 0; e < 4; ++e) s[tb][i + e] *= x[e];
                 }
         // The running maximum only moves when a score passes it by 2^8: weights up to
         // 256 are as exact, and most steps leave the sums as they are.
+        float top = -INFINITY;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            float top = -INFINITY;
+        for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-            for (int tb = 0; tb < TB; ++tb)
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[tb][i]);
+        top *= a.scale2;
+        if (__any(top > m + 8.0f)) {
+            top = fmaxf(fmaxf(top, __shfl_xor(top, 32)), m);
+            const float f = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+            m = top;
+            if (j0 != job.begin) {   // (zeros so far)
+                l *= f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[nb][tb][i]);
-            top *= a.scale2;
-            if (__any(top > m[nb] + 8.0f)) {
-                top = fmaxf(fmaxf(top, __shfl_xor(top, 32)), m[nb]);
-                const float f = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[nb] - top);
-                m[nb] = top;
-                if (j0 != job.begin) {   // (zeros so far)
-                    l[nb] *= f;
-#pragma unroll
-                    for (int db = 0; db < DB; ++db) o[nb][db] *= f;
-                }
+                for (int db = 0; db < DB; ++db) o[db] *= f;
             }
         }
         // Group g of 16 slots: its weights are computed between the products of the
         // group before, and its values read there.
         constexpr int GROUPS = TB * 2;
-        float base[NB];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) base[nb] = m[nb] == -INFINITY ? 0.0f : -m[nb];
+        const float base = m == -INFINITY ? 0.0f : -m;
         constexpr int VB = DB < 8 ? 2 : 1;   // (with 8 products a group, the next group's values take the places of those used)
-        u4 v[VB][DB], p[2][NB][WP];
+        u4 v[VB][DB], p[2][WP];
         auto read_v = [&](int g, int db) {
             const char *at = here + v_at[db] + g * 16 * PC * 16;
             const u2 x = read_turned(at), y = read_turned(at + 8 * PC * 16);
@@ -560,20 +538,17 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
         };
         auto weigh = [&](int g, int i) {   // two weights
             const int tb = g / 2, e = g % 2 * 8 + i * 2;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                float w0 = __builtin_amdgcn_exp2f(fmaf(s[nb][tb][e], a.scale2, base[nb]));
-                float w1 = __builtin_amdgcn_exp2f(fmaf(s[nb][tb][e + 1], a.scale2, base[nb]));
-                l[nb] += w0 + w1;
-                if constexpr (I8) {
-                    const f2 x = *reinterpret_cast<const f2 *>(scales + KT + tb * 32 + (e / 4) * 8 + e % 4);
-                    w0 *= x[0], w1 *= x[1];
-                }
-                uint32_t x[WP];
-                split2<WP>(w0, w1, x);
-#pragma unroll
-                for (int n = 0; n < WP; ++n) p[g & 1][nb][n][i] = x[n];
+            float w0 = __builtin_amdgcn_exp2f(fmaf(s[tb][e], a.scale2, base));
+            float w1 = __builtin_amdgcn_exp2f(fmaf(s[tb][e + 1], a.scale2, base));
+            l += w0 + w1;
+            if constexpr (I8) {
+                const f2 x = *reinterpret_cast<const f2 *>(scales + KT + tb * 32 + (e / 4) * 8 + e % 4);
+                w0 *= x[0], w1 *= x[1];
             }
+            uint32_t x[WP];
+            split2<WP>(w0, w1, x);
+#pragma unroll
+            for (int n = 0; n < WP; ++n) p[g & 1][n][i] = x[n];
         };
 #pragma unroll
         for (int db = 0; db < DB; ++db) read_v(0, db);
@@ -586,9 +561,7 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
             for (int db = 0; db < DB; ++db) {
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int n = 0; n < WP; ++n) o[nb][db] = mfma32(v[g % VB][db], p[g & 1][nb][n], o[nb][db]);
+                for (int n = 0; n < WP; ++n) o[db] = mfma32(v[g % VB][db], p[g & 1][n], o[db]);
                 if (g + 1 < GROUPS) {
                     read_v(g + 1, db);
 #pragma unroll
@@ -612,38 +585,30 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
             a.lse[job.lse_at + (int64_t)t * a.hq + g] = M == -INFINITY ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
         }
     };
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        l[nb] += __shfl_xor(l[nb], 32);
-        // A NaN score is in l, but maxima drop it.  A maximum of infinity takes it
-        // through every join: exp2(inf - inf) is NaN, other parts count 0 beside it.
-        if (l[nb] != l[nb]) m[nb] = INFINITY;
-    }
+    l += __shfl_xor(l, 32);
+    // A NaN score is in l, but maxima drop it.  A maximum of infinity takes it
+    // through every join: exp2(inf - inf) is NaN, other parts count 0 beside it.
+    if (l != l) m = INFINITY;
     // (slots that do not count give NaN, too, to a row whose queries are not finite)
     const bool none = any == 0;
-    if (none)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) m[nb] = -INFINITY, l[nb] = 0.0f;
+    if (none) m = -INFINITY, l = 0.0f;
     __syncthreads();   // (the last step's LDS is read no more)
     if constexpr (WIDE) {
         constexpr bool H = BF16;               // rows of out in bf16, parts in fp32
         constexpr int OP = C::OP;
-        char *mine = lds + wave * NB * 32 * OP * 4;
+        char *mine = lds + wave * 32 * OP * 4;
+        const float f = parts ? 1.0f : m == -INFINITY ? 0.0f : BF16 ? __builtin_amdgcn_rcpf(l) : 1.0f / l;
+        if (hf == 0 && row < job.R) put_stat(row, m, l);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const float f = parts ? 1.0f : m[nb] == -INFINITY ? 0.0f : BF16 ? __builtin_amdgcn_rcpf(l[nb]) : 1.0f / l[nb];
-            if (hf == 0 && row[nb] < job.R) put_stat(row[nb], m[nb], l[nb]);
+        for (int db = 0; db < DB; ++db)
 #pragma unroll
-            for (int db = 0; db < DB; ++db)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int at = (nb * 32 + col) * OP + db * 32 + i * 8 + hf * 4;
-                    const f4 x = none ? f4{0, 0, 0, 0} : f4{o[nb][db][4 * i], o[nb][db][4 * i + 1], o[nb][db][4 * i + 2], o[nb][db][4 * i + 3]} * f;
-                    if (H && !parts) store4<true>(mine, at, x);
-                    else store4<false>(mine, at, x);
-                }
-        }
-        const int first = job.row0 + wave * NB * 32, n = min(NB * 32, job.R - first);   // (below 1: none)
+            for (int i = 0; i < 4; ++i) {
+                const int at = col * OP + db * 32 + i * 8 + hf * 4;
+                const f4 x = none ? f4{0, 0, 0, 0} : f4{o[db][4 * i], o[db][4 * i + 1], o[db][4 * i + 2], o[db][4 * i + 3]} * f;
+                if (H && !parts) store4<true>(mine, at, x);
+                else store4<false>(mine, at, x);
+            }
+        const int first = job.row0 + wave * 32, n = min(32, job.R - first);   // (below 1: none)
         if (H && !parts) {
             for (int x = lane; x < n * PC; x += 64) {
                 const int r = x / PC, d = (x - r * PC) * 8;
@@ -662,18 +627,18 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
             }
         }
     } else {
-        static_assert(WIDE || (NB == 1 && C::RW == 1), "waves along the tokens have the same 32 rows");
+        static_assert(WIDE || C::RW == 1, "waves along the tokens have the same 32 rows");
         float *so = reinterpret_cast<float *>(lds), *st = so + C::TW * 32 * C::OP;
         if (hf == 0) {
-            st[(wave * 32 + col) * 2] = m[0];
-            st[(wave * 32 + col) * 2 + 1] = l[0];
+            st[(wave * 32 + col) * 2] = m;
+            st[(wave * 32 + col) * 2 + 1] = l;
         }
 #pragma unroll
         for (int db = 0; db < DB; ++db)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 *reinterpret_cast<f4 *>(so + (wave * 32 + col) * C::OP + db * 32 + i * 8 + hf * 4) =
-                    none ? f4{0, 0, 0, 0} : f4{o[0][db][4 * i], o[0][db][4 * i + 1], o[0][db][4 * i + 2], o[0][db][4 * i + 3]};
+                    none ? f4{0, 0, 0, 0} : f4{o[db][4 * i], o[db][4 * i + 1], o[db][4 * i + 2], o[db][4 * i + 3]};
         __syncthreads();
         const int rows = min(32, job.R - job.row0);
         // Parts that another launch left for these rows join here.  A wave a row: lane
@@ -1020,7 +985,7 @@ void by_dim(int DP, F f) {
     else f(std::integral_constant<int, 256>{});
 }
 template <int DP, bool B, Source S, int WAVES>
-using Narrow = Shape<DP, B, 1, 1, WAVES, S>;
+using Narrow = Shape<DP, B, 1, WAVES, S>;
 // calls f with the shape of a narrow kind (those that kind_of() gives)
 template <int DP, bool B, Source S, class F>
 void narrow(Kind k, F f) {
@@ -1137,7 +1102,7 @@ int launch_cross_attention(const rq_states *st, const void *q, int bf16, int64_t
     auto run = [&](auto dp, auto b) {
         constexpr int DP = decltype(dp)::value;
         constexpr bool B = decltype(b)::value;
-        using W = Shape<DP, B, 1, 4, 1, STATES>;
+        using W = Shape<DP, B, 4, 1, STATES>;
         if (p.kind == WIDE) err = go<W>(cross_kernel<W>, p.grid, a, s);
         else narrow<DP, B, STATES>(p.kind, [&](auto n) { err = go<decltype(n)>(cross_kernel<decltype(n)>, p.grid, a, s); });
     };
@@ -1178,7 +1143,7 @@ int launch_prefix_attention(const rq_kv_cache *c, const int32_t *prefix_table, i
         constexpr int DP = decltype(dp)::value;
         constexpr bool B = decltype(b)::value;
         constexpr Source S = decltype(src)::value;
-        using W = Shape<DP, B, 1, 4, 1, S>;
+        using W = Shape<DP, B, 4, 1, S>;
         if (p.grid > 0) {
             if (p.kind == WIDE) err = go<W>(prefix_kernel<W>, p.grid, a, s);
             else narrow<DP, B, S>(p.kind, [&](auto n) { err = go<decltype(n)>(prefix_kernel<decltype(n)>, p.grid, a, s); });
