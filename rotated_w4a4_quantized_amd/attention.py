@@ -270,6 +270,8 @@ class DiffusionAttention:
             raise ValueError(f"expected modulations [{self.batch}][5][{x.shape[-1]}], got {tuple(mod.shape)}")
         if x.shape != self.h.shape:
             raise ValueError(f"expected tokens {tuple(self.h.shape)}, got {tuple(x.shape)}")
+        if x.dtype is not self.h.dtype:
+            raise TypeError(f"the block's stream is {self.h.dtype}, got {x.dtype}")
         shift, scale, gate, mlp_shift, mlp_scale = mod.unbind(1)
         s = dict(stream=stream)
         rq.block_norm(x, self.z, self.layer_norm, mod=rq.Modulation(shift=shift, scale=scale, per=self.tokens), **s)

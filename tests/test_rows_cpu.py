@@ -1,4 +1,4 @@
-"""Attention to shared keys without a GPU: that the GPU tests' cases reach every
+"""Attention to shared keys, and the diffusion block on it, without a GPU: that the GPU tests' cases reach every
 kernel that a call can (by the rules of choice written out in tests/_rows.py, which
 the library's workspace sizes confirm)."""
 import ctypes
@@ -8,7 +8,7 @@ import pytest
 from rotated_w4a4_quantized_amd import rq
 from tests import _rows as R
 from tests import test_blocks_gpu, test_rows_gpu
-from tests.test_blocks_cpu import BF16, F32, SHAPE, cache, call_cross, call_prefix, ref, states
+from tests.test_blocks_cpu import BF16, F32, SHAPE, _weights, cache, call_cross, call_prefix, ref, states
 
 torch = pytest.importorskip("torch")
 
@@ -59,3 +59,20 @@ def test_scales_that_overflow_are_refused(scale):
     assert call_cross(scale=scale) == SHAPE
     assert call_prefix(scale=scale) == SHAPE
     assert call_cross(states(batch=0), scale=2.0 ** 127) == 0 and call_prefix(cache(batch=0), scale=-2.0 ** 127) == 0
+
+
+def test_diffusion_block_refuses_a_stream_of_another_type(monkeypatch):
+    """Before anything runs."""
+    from rotated_w4a4_quantized_amd import attention
+    hidden, heads, D, batch, tokens, caption = 128, 2, 64, 2, 5, 64
+    inner, calls = heads * D, []
+    for name in ("rotate_quant", "w4a4_linear", "qk_norm_rope", "block_norm", "cross_attention"):
+        monkeypatch.setattr(rq, name, lambda *a, _n=name, **k: calls.append(_n))
+    blk = attention.DiffusionAttention(*_weights((3 * inner, hidden), (hidden, inner), (inner, hidden), (2 * inner, caption), (hidden, inner)),
+                                       heads, D, batch, tokens, 7, device="cpu")
+    blk.set_caption(torch.zeros(batch, 3, caption, dtype=torch.bfloat16))
+    calls.clear()
+    for dtype in (torch.float32, torch.float16):
+        with pytest.raises(TypeError):
+            blk.step(torch.zeros(batch * tokens, hidden, dtype=dtype), torch.zeros(batch, 5, hidden))
+    assert not calls
