@@ -932,7 +932,8 @@ rq_status rq_cross_attention_workspace_bytes(const rq_states *states, int64_t qu
  *   Rows of q and out must start 16-byte aligned.
  * Sums and softmax statistics are fp32; the weights enter the product with the values
  * with 16 bits for bf16 results and 24 for fp32 ones, as rq_paged_attention's.  The
- * same inputs give the same bits.
+ * same inputs give the same bits; a row's last bits can change with the call's other
+ * rows and sizes.
  * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_DTYPE, RQ_ERR_ALIGN, RQ_ERR_HIP.
  */
 rq_status rq_cross_attention(const rq_states *states, const void *q, int32_t dtype, int64_t q_ld,
@@ -956,8 +957,10 @@ rq_status rq_prefix_attention_workspace_bytes(const rq_kv_cache *cache, int32_t 
  * table as ever (its entries of pages that lie wholly below prefix are not
  * read; a page that prefix ends in has the sequence's own copy).  The result is
  * rq_paged_attention's with prefix_table's pages in front of every row of the
- * table.  A sequence with lens[b] < prefix or lens[b] < 1 has no token in the
- * batch: its out is 0 and its lse -infinity.
+ * table, up to the order of fp32 sums: the same inputs give the same bits, but a
+ * sequence's last bits can change with the batch's other sequences.  A sequence with
+ * lens[b] < prefix or lens[b] < 1 has no token in the batch: its out is 0 and its lse
+ * -infinity.
  * Arguments as rq_paged_attention, and
  *   scale      at most 2^127 in magnitude
  *   prefix_table  device int32 [ceil(prefix / page)], 16-byte aligned (NULL when

@@ -4,7 +4,8 @@
 //
 // with post and pre an RMS norm, a layer norm or nothing.  x and y are read once,
 // h and z written once: HBM bounds it (32760 x 1536, fp32 stream, 604 MB in 124 us: 4.9
-// TB/s, a copy's rate; 8192 x 1152 in bf16 75 MB in 18 us, of which 15 are the bytes').
+// TB/s, a copy's rate; 8192 x 1152 in bf16 75 MB in 18 us, of which 15 are the bytes'),
+// but for the widths whose registers do not suffice (below).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -78,8 +79,12 @@ __device__ __forceinline__ void store8(void *p, int64_t at, const float (&f)[8])
 // tokens walk by (read again for each token they would be more bytes, from the caches,
 // than the rows).  The next token's rows are on their way meanwhile.  Two waves a SIMD:
 // with one, 8192 x 1152 took 25 us against 20, 32760 x 1536 132 against 130; three have
-// too few registers (63 and 307).  Rows of up to 2048 values take one wave and no
-// barrier.  RB, IB: x and h, y and z are bf16 (else fp32).
+// too few registers (63 and 307).  They hold up to three pieces (at most 32 registers
+// are spilled); with four, widths of 1537 to 2048, 6145 to 8192 and 12289 to 16384, 99 to
+// 177 are, and come from scratch for every token: 33.5 M bf16 values of the stream, modulated
+// and gated, take 88 us at a width of 2048, 94 at 8192 and 106 at 16384, against 57 at 1536,
+// 56 at 4096 and 57 at 12288 (fp32: 170, 181, 180 against 116, 107, 117).  Rows of up to
+// 2048 values take one wave and no barrier.  RB, IB: x and h, y and z are bf16 (else fp32).
 template <bool RB, bool IB, int WAVES, int CH>
 __global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) __attribute__((amdgpu_waves_per_eu(2))) block_norm_kernel(Args a) {
     constexpr int GROUPS = WAVES == 1 ? 4 : 1;   // tokens of a workgroup at a time
@@ -142,8 +147,7 @@ __global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) __attribute__((
         const float none = ok ? 0.0f : NAN;
         const int64_t base = ok ? (int64_t)r * a.mod_ld : 0;
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
-{
+        for (int c = 0; c < CH; ++c) {
             const int k = in[c] ? at[c] : 0;
             float g[8], s[8], b[8], w[8];
             auto vec = [&](const float *p, int64_t from, float other, float (&v)[8]) {

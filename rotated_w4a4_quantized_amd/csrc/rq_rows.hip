@@ -8,15 +8,16 @@
 // one problem: row r is token r / G, head r % G.
 //
 // Many rows are bound by the matrix cores and by the vector units beside them: a block
-// of 32 rows x 32 keys x 128 takes 16 products of 32 cycles and some 75 other
+// of 32 rows x 32 keys x 128 takes 24 products of 32 cycles and some 115 other
 // instructions (half the maximum, exponent's argument, exponential at twice an
-// instruction's time, sum, half a conversion for each of its 16 registers, and the
-// step's own).  9216 x 9216 tokens, 12 heads of 128, run at 955 to 980 TFLOP/s (540 us;
-// a large bf16 product of the library reaches 1200), where 864 row tiles on 512 places
-// leave a sixth of the second round empty; 4 x 4096 x 1280 at 940.  Short keys are bound
-// by what every workgroup starts and ends with (5 us: arguments, keys and queries,
-// results), of which as many as fit run side by side.  Few rows are bound by HBM: 77
-// queries on 201 MB of keys and values 40 us (5.0 TB/s) and 7 us of joining.
+// instruction's time, sum, conversion and two for what the weight's first part leaves,
+// for each of its 16 registers, and the step's own).  9216 x 9216 tokens, 12 heads of
+// 128, take 720 us: 725 TFLOP/s, of products with the weights' second part 1090 (a large
+// bf16 product of the library reaches 1220), where 864 row tiles on 512 places leave a
+// sixth of the second round empty; 4 x 4096 x 1280 run at 730.  Short keys are bound by
+// what every workgroup starts and ends with (5 us: arguments, keys and queries, results),
+// of which as many as fit run side by side.  Few rows are bound by HBM: 77 queries on 201
+// MB of keys and values 44 us (4.5 TB/s) and 7 us of joining.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -223,9 +224,9 @@ struct Shape {
 // (24 bits).  Weights enter as two bf16 parts (16 bits) for bf16 outputs and as three
 // for fp32 ones; sums and statistics are fp32.  One part for bf16 outputs would be off by
 // as much as the output's own rounding (from 64 bits 0.0025 relative in all, with two
-// 0.0017, as the rounding alone); the second costs 33% where the products are the bound
-// (9216 x 9216 tokens, 12 heads of 128: 545 -> 727 us), 8 to 17% on a caption's keys and at
-// most 10% elsewhere.
+// 0.0017, as the rounding alone); the second costs a third where the products are the
+// bound (9216 x 9216 tokens, 12 heads of 128: 541 -> 720 us; 4 x 4096 x 1280, 16 heads of 64:
+// 100 -> 143), 8 to 18% on a caption's keys and at most 11% elsewhere.
 template <class C>
 __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char *lds) {
     constexpr int DP = C::DP, KT = C::KT, TB = C::TB, PC = C::PC;
@@ -464,7 +465,7 @@ __device__ __forceinline__ void attend_rows(const Args &a, const Job &job, char 
                     for (int n = 0; n < QP; ++n) s[tb] = mfma32(k[ks], q[ks][n], s[tb]);
                     if (tb + 1 < TB) read_k(tb + 1, ks);
                     // the next step's loads, spread: at once, a workgroup's would fill the way to LDS
-                    // and its waves wait (32760 queries x 512 keys 140 -> 129 us, heads of 256 260 -> 223)
+                    // and its waves wait (32760 queries x 512 keys 173 -> 161 us, heads of 256 297 -> 266)
                     if constexpr (SPREAD) {
                         const int slot = tb * KS + ks;
 #pragma unroll
@@ -742,7 +743,7 @@ __global__ void __launch_bounds__(C::threads) __attribute__((amdgpu_waves_per_eu
     if (a.longest_first) {
         // Each XCD takes its share of the tiles of every sequence, the longest sequence's
         // first: the last workgroups to start are short (5 uneven sequences of 333 fp32
-        // queries 45 -> 40 us, 4 of 4096 queries, 300 keys at most, 42 -> 41).
+        // queries 45 -> 40 us; 4 of 4096 queries, 300 keys at most, 44.8 -> 44.4).
         const int x = (uint32_t)block % 8, l = (uint32_t)block / 8, rank = a.by_share.of(l), lane = threadIdx.x & 63;
         const int length = lane < a.batch ? min(max(a.lens[lane], 0), a.keys) : -1;
         int mine = 0;
@@ -910,7 +911,7 @@ __global__ void __launch_bounds__(kJoin) join_rows_kernel(Args a) {
 
 // The same for rows of a few parts: a thread takes a quad of a row, all of its
 // parts' statistics and outputs in flight at once (5 uneven sequences of 333 fp32
-// queries, 26640 rows of 4 parts: the call 39.8 -> 37.6 us).
+// queries, 26640 rows of 4 parts: the call 41.0 -> 40.1 us).
 constexpr int kFew = 8;
 template <bool BF16, bool PREFIX>
 __global__ void __launch_bounds__(kJoin) join_few_kernel(Args a) {
@@ -957,8 +958,8 @@ void join(const Args &a, hipStream_t s) {
 // The kernel's shape: many rows divide over the waves, few leave the waves the
 // tokens.  There, four waves a workgroup (heads of 65 to 128: one workgroup a CU) where a
 // CU has no more than one step of them to do, two (two a CU, which overlap) beyond: 5
-// sequences behind 1999 int8 tokens 18.4 us with four, 23.6 with two; 64 behind 16384
-// 59.4 and 53.3; 256 of 500 keys 42.6 and 36.3; 1 x 32760 keys 49.3 and 45.7.
+// sequences behind 1999 int8 tokens 21.0 us with four, 25.8 with two; 64 behind 16384
+// 65.0 and 60.4; 256 of 500 keys 45.1 and 38.2; 1 x 32760 keys 49.9 and 46.4.
 enum Kind { NARROW2 = 2, NARROW4 = 4, WIDE = 0 };
 constexpr int kNarrow = 32;
 Kind kind_of(int DP, int64_t R, int64_t problems, int64_t keys) {
@@ -971,9 +972,9 @@ int step_of(Kind k) { return k == WIDE ? 64 : k * 32; }
 
 // Parts of a problem of `keys` where `jobs` workgroups take one each, of `least`
 // steps at the least: as many as make two workgroups a CU; fp32 calls with heads up to
-// 64, whose steps take three times as long, four, so that uneven ones even out (5 uneven
-// sequences of 333 x 1999 54 -> 45 us; heads of 128, one workgroup a CU, lose: 4 of 1000 x
-// 2000 80 -> 104; and bf16 pays more for the parts: 77 queries x 32760 56 -> 67).
+// 64, whose steps take longer, four, so that uneven ones even out (5 uneven sequences of
+// 333 x 1999 47 -> 40 us; heads of 128, one workgroup a CU, lose: 4 of 1000 x 2000 80 -> 100;
+// and bf16 pays more for the parts: 77 queries x 32760 56 -> 66).
 int parts_of(int64_t jobs, int64_t keys, int step, int least, bool twice) {
     const int64_t steps = (keys + step - 1) / step, enough = (twice ? 2 : 1) * (int64_t)device_cus();
     if (jobs >= enough || jobs < 1) return 1;
