@@ -838,7 +838,8 @@ typedef struct rq_modulation {
  * fp32 throughout:
  *   h = alpha x + beta gate (.) post(y);   z = pre(h) (.) (1 + scale) + shift
  * h and z are rounded once each (z is computed from h before its rounding).
- * Means of squares are fp32: with eps 0, rows below 2^-63 lose digits.
+ * Means of squares are fp32: with eps 0, rows below 2^-63 lose digits, and values of
+ * 2^56 and more may overflow them.
  * Arguments:
  *   post, pre  norms, each may be NULL (none).  post needs y, pre needs z.
  *   mod        modulations or NULL (gate 1, shift 0, scale 0)
